@@ -319,6 +319,113 @@ MLA_API int mla_append_kv_fp8(mla_handle_t h, int32_t batch, int32_t d_model, co
                       int32_t num_pages, mla_stream_t stream);
 
 /*
+ * What stands between the residual stream and the calls above, with int8 codes between a norm and
+ * a product ([V3-walk] section 4.4: activations quantised per token on their way into a product,
+ * weights quantised once, high-precision accumulation; the int8 format is this library's). A layer
+ * around the decode step runs
+ *   mla_add_norm_q8 -> mla_linear_q8 with [W^DQ ; W^DKV ; W^KR] -> mla_add_norm_q8 on the W^DQ
+ *   columns (no residual) -> mla_linear_q8 with W^UQ and with W^QR; mla_append_rows on the other
+ *   576 columns; mla_decode_step; mla_quantize_rows -> mla_linear_q8 with W^O.
+ * These five calls use the handle's device whichever device is current, and no workspace: several
+ * may run at once. Rows may lie apart (a stride in elements between rows, at least the row's
+ * length); where a call says nothing else a pointer needs its elements' alignment only. n_rows 0
+ * is valid and does nothing. Outputs must not overlap inputs, but for those named.
+ */
+enum {
+  MLA_BF16 = 0,
+  MLA_F32 = 1
+};
+
+/*
+ * Residual addition, RMSNorm and int8 quantisation with one scale per row:
+ *   r      = x + residual (fp32; r = x without one);  residual_out = r in the residual's type
+ *   rstd   = 1 / sqrt(mean(r^2) + rms_eps)
+ *   y      = r * rstd * gamma                                                      (bf16)
+ *   codes  = the integers nearest to 127 t / m, ties to even, t = r * gamma (fp32), m = max|t|
+ *   scales = m * rstd / 127, so that codes * scales is the normalised row to half a code
+ * A row of zeros gets codes 0 and scale 0; a row with an infinity or a NaN in t gets codes 0 and a
+ * NaN scale. Codes depend on no sum: they are the same on every run and for any layout.
+ * d             1..16384
+ * x             [n_rows, d] of x_type (MLA_BF16 or MLA_F32), rows x_stride elements apart
+ * residual, residual_out  [n_rows, d] of residual_type, both or neither NULL; residual_out may be
+ *               the residual itself (same pointer and stride)
+ * gamma         bf16 [d];  rms_eps >= 0 and finite
+ * y             bf16 [n_rows, d], or NULL: not wanted; may be x itself where x is bf16
+ * codes, scales int8 [n_rows, d] and fp32 [n_rows], or both NULL: not wanted (y is wanted then).
+ *               mla_linear_q8 reads codes that are 16-byte aligned, rows a multiple of 16 apart.
+ * Rows that are 16-byte aligned everywhere (codes 8-byte) with d a multiple of 8 are moved 16
+ * bytes at a time.
+ * Errors: MLA_ERR_INVALID_ARG for NULL pointers, a bad type, size, stride, rms_eps or alignment;
+ * MLA_ERR_UNSUPPORTED for d > 16384 or n_rows >= 2^31.
+ */
+MLA_API int mla_add_norm_q8(mla_handle_t h, int64_t n_rows, int32_t d, const void* x, int32_t x_type,
+                    int64_t x_stride, const void* residual, int64_t residual_stride, void* residual_out,
+                    int64_t residual_out_stride, int32_t residual_type, const void* gamma, float rms_eps,
+                    void* y, int64_t y_stride, int8_t* codes, int64_t codes_stride, float* scales,
+                    mla_stream_t stream);
+
+/*
+ * The codes and scales of x itself (as above with t = x and rstd = 1): the heads' outputs on their
+ * way into W^O, or a weight [n, k], whose rows are output channels. Errors as for mla_add_norm_q8.
+ */
+MLA_API int mla_quantize_rows(mla_handle_t h, int64_t n_rows, int32_t d, const void* x, int32_t x_type,
+                    int64_t x_stride, int8_t* codes, int64_t codes_stride, float* scales,
+                    mla_stream_t stream);
+
+/*
+ * The product of int8 rows and an int8 weight, with a scale per row and per output channel:
+ *   out[i,j] = (sum_l codes[i,l] * w_codes[j,l]) * w_scales[j] * scales[i]
+ * The sum is exact (32-bit integers); it is rounded to fp32, and so is each of the two products,
+ * then once to out_type. A row with a NaN scale gives NaN. An infinite or NaN scale does not
+ * reach other rows or channels.
+ * k        1..131071;  n_rows, n at most 2^20
+ * codes    int8 [n_rows, k] (any value, -128 too), 16-byte aligned, codes_stride a multiple of 16
+ * w_codes  int8 [n, k], an nn.Linear weight's layout, aligned likewise
+ * scales   fp32 [n_rows];  w_scales fp32 [n]
+ * out      [n_rows, n] of out_type, rows out_stride elements apart
+ * Errors: MLA_ERR_INVALID_ARG for NULL pointers, a bad type, size, stride or alignment;
+ * MLA_ERR_UNSUPPORTED beyond the limits above or for strides over 2^32.
+ */
+MLA_API int mla_linear_q8(mla_handle_t h, int32_t n_rows, int32_t k, int32_t n, const int8_t* codes,
+                    int64_t codes_stride, const float* scales, const int8_t* w_codes, int64_t w_stride,
+                    const float* w_scales, void* out, int32_t out_type, int64_t out_stride,
+                    mla_stream_t stream);
+
+/*
+ * mla_append_kv for rows that are projected already, x = [W_DKV ; W_KR] h (576 values):
+ *   c^KV row = x[0:512] / sqrt(mean(x[0:512]^2) + rms_eps) * gamma;  k^R row = RoPE(x[512:576])
+ * with any number of new tokens per sequence: rows row_starts[b] .. row_starts[b+1]-1 of x are the
+ * last ones of sequence b, in order, so row i goes to position kv_lens[b] - row_starts[b+1] + i
+ * and is rotated there. Rows before row_starts[0] or from row_starts[batch] on belong to no
+ * sequence (a padded batch) and write nothing, nor does a sequence without rows, whose kv_lens
+ * entry is not looked at.
+ * n_rows     rows of x (>= 0)
+ * x          [n_rows, 576] of x_type, 16-byte aligned, x_stride * element size a multiple of 16
+ * row_starts int32 [batch + 1], not decreasing; NULL: q_len rows per sequence in order
+ *            (n_rows = batch * q_len)
+ * gamma, rms_eps, the cache, kv_lens, page_table: as for mla_append_kv. No two rows may go to the
+ *            same cache row. k_r needs c_kv's alignment.
+ * A row whose position lies before 0, whose kv_lens entry is over max_kv_len, or whose page-table
+ * entry is outside 0..num_pages-1, sets the device error word and is skipped; the other rows are
+ * written. Errors: MLA_ERR_INVALID_ARG as for mla_append_kv, and for a bad x_type or x_stride.
+ */
+MLA_API int mla_append_rows(mla_handle_t h, int32_t batch, int32_t n_rows, const void* x, int32_t x_type,
+                    int64_t x_stride, const void* gamma, float rms_eps, void* c_kv, void* k_r,
+                    int64_t row_stride, int64_t seq_stride, const int32_t* kv_lens,
+                    const int32_t* row_starts, const int32_t* page_table, int32_t max_pages,
+                    int32_t num_pages, mla_stream_t stream);
+
+/*
+ * mla_append_rows into a quantised cache (codes and exponents as mla_append_kv_fp8 writes them: the
+ * smallest power of two with max|row| / 2^e <= 448, values rounded to the nearest E4M3 code).
+ */
+MLA_API int mla_append_rows_fp8(mla_handle_t h, int32_t batch, int32_t n_rows, const void* x, int32_t x_type,
+                    int64_t x_stride, const void* gamma, float rms_eps, void* kv_codes, int8_t* kv_exp,
+                    int64_t row_stride, int64_t seq_stride, const int32_t* kv_lens,
+                    const int32_t* row_starts, const int32_t* page_table, int32_t max_pages,
+                    int32_t num_pages, mla_stream_t stream);
+
+/*
  * mla_decode_attn for callers that cannot allocate device memory. The pages have no
  * counterpart to this call: it exists for library users whose device memory is owned by
  * someone else (a serving engine that has reserved nearly all of HBM for its own KV-cache

@@ -29,6 +29,8 @@ ERR_BAD_KV_LEN = 1 << 2
 ROW = 576
 D_LATENT = 512
 
+ROW_TYPES = {torch.bfloat16: 0, torch.float32: 1}   # MLA_BF16, MLA_F32
+
 
 class MlaConfig(ctypes.Structure):
     _fields_ = [
@@ -76,6 +78,14 @@ SIGNATURES = {
     "mla_merge_partials": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _P, _P]),
     "mla_append_kv": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _P, ctypes.c_float, _P, _P,
                                      _I64, _I64, _P, _P, _I32, _I32, _P]),
+    "mla_add_norm_q8": (ctypes.c_int, [_P, _I64, _I32, _P, _I32, _I64, _P, _I64, _P, _I64, _I32, _P,
+                                       ctypes.c_float, _P, _I64, _P, _I64, _P, _P]),
+    "mla_quantize_rows": (ctypes.c_int, [_P, _I64, _I32, _P, _I32, _I64, _P, _I64, _P, _P]),
+    "mla_linear_q8": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _I64, _P, _P, _I64, _P, _P, _I32, _I64, _P]),
+    "mla_append_rows": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _I64, _P, ctypes.c_float, _P, _P, _I64, _I64,
+                                       _P, _P, _P, _I32, _I32, _P]),
+    "mla_append_rows_fp8": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _I64, _P, ctypes.c_float, _P, _P, _I64,
+                                           _I64, _P, _P, _P, _I32, _I32, _P]),
     "mla_decode_attn_noalloc": (ctypes.c_int, [_I32, ctypes.c_float, _I32, _I64, _I32, _P, _P, _P,
                                                _I64, _I64, _P, _P, _I32, _I32, _P, _P, _P, _P]),
     "mla_check_device_errors": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
@@ -147,6 +157,10 @@ def _need(t: torch.Tensor, dtype, name: str) -> None:
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor, got "
                          f"{t.dtype} on {t.device} (contiguous={t.is_contiguous()})")
+
+
+def _shape(t: torch.Tensor) -> str:
+    return f"{t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}"
 
 
 class MlaDecode:
@@ -437,6 +451,186 @@ class MlaDecode:
         _check(self._lib.mla_apply_wuv_fp8(self._h, B, _ptr(latent), _ptr(w_uv_codes), _ptr(w_uv_exp),
                                            _ptr(out), _stream(stream)), "mla_apply_wuv_fp8")
         return out
+
+    # -- around the decode step: int8 rows, the int8 projection, projected rows ----------
+    def _here(self, stream):
+        """The stream to launch on: the current one of the handle's device unless given."""
+        return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else stream.cuda_stream
+
+    def _rows(self, t: torch.Tensor, name: str, dtypes, shape=None) -> int:
+        """The stride between the rows of a [rows, d] tensor on the handle's device."""
+        if t.device.type != "cuda" or t.device.index != self.device or t.dtype not in dtypes or t.dim() != 2 or \
+                (t.shape[1] > 1 and t.stride(1) != 1) or (shape is not None and t.shape != shape):
+            raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dtypes)} "
+                             f"{'[rows, d]' if shape is None else tuple(shape)} with unit inner stride "
+                             f"on cuda:{self.device}, got {_shape(t)}")
+        stride = t.stride(0)
+        if t.shape[0] > 1 and stride < t.shape[1]:
+            raise ValueError(f"{name}: rows overlap, got {_shape(t)}")
+        return stride if t.shape[0] > 1 and stride > t.shape[1] else t.shape[1]
+
+    def _flat(self, t: torch.Tensor, name: str, dtype, n: int) -> None:
+        if t.device.type != "cuda" or t.device.index != self.device or t.dtype != dtype or t.dim() != 1 or \
+                t.shape[0] != n or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous {dtype} [{n}] tensor on cuda:{self.device}, "
+                             f"got {_shape(t)}")
+
+    def _new_codes(self, rows: int, d: int, codes, scales, x):
+        """Codes and scales to write (rows of new codes are a multiple of 16 bytes apart)."""
+        if codes is None:
+            codes = torch.empty((rows, (d + 15) // 16 * 16), dtype=torch.int8, device=x.device)
+            codes = codes if d % 16 == 0 else codes[:, :d]
+        if scales is None:
+            scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+        stride = self._rows(codes, "codes", (torch.int8,), (rows, d))
+        self._flat(scales, "scales", torch.float32, rows)
+        return codes, stride, scales
+
+    @staticmethod
+    def _code_stride(t: torch.Tensor, stride: int) -> int:
+        """One row of codes has no stride of its own: any multiple of 16 will do."""
+        return stride if t.shape[0] > 1 else (stride + 15) // 16 * 16
+
+    def add_norm_q8(self, x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                    eps: float = 1e-6, want_y: bool = False, residual_out: Optional[torch.Tensor] = None,
+                    codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                    y: Optional[torch.Tensor] = None, stream=None):
+        """r = x + residual; RMSNorm of r with weight gamma; its int8 codes with a scale per row.
+        x [rows, d] bf16 or fp32 (rows may lie apart), residual likewise (its own type), gamma [d]
+        bf16. Returns (codes int8 [rows, d], scales fp32 [rows], residual_out, y): residual_out is
+        r in the residual's type (a new tensor unless given; `residual` itself is allowed), None
+        without a residual; y is the normalised row in bf16, None unless wanted or given."""
+        rows, d = x.shape if x.dim() == 2 else (-1, -1)
+        x_stride = self._rows(x, "x", ROW_TYPES)
+        self._flat(gamma, "gamma", torch.bfloat16, d)
+        res_stride = out_stride = y_stride = res_type = 0
+        if residual is not None:
+            res_stride = self._rows(residual, "residual", ROW_TYPES, x.shape)
+            if residual_out is None:
+                residual_out = torch.empty((rows, d), dtype=residual.dtype, device=x.device)
+            out_stride = self._rows(residual_out, "residual_out", (residual.dtype,), x.shape)
+            res_type = ROW_TYPES[residual.dtype]
+        elif residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        codes, codes_stride, scales = self._new_codes(rows, d, codes, scales, x)
+        if y is None and want_y:
+            y = torch.empty((rows, d), dtype=torch.bfloat16, device=x.device)
+        if y is not None:
+            y_stride = self._rows(y, "y", (torch.bfloat16,), x.shape)
+        if rows > 0:
+            _check(self._lib.mla_add_norm_q8(
+                self._h, rows, d, x.data_ptr(), ROW_TYPES[x.dtype], x_stride,
+                None if residual is None else residual.data_ptr(), res_stride,
+                None if residual is None else residual_out.data_ptr(), out_stride, res_type, gamma.data_ptr(), eps,
+                None if y is None else y.data_ptr(), y_stride, codes.data_ptr(), codes_stride, scales.data_ptr(),
+                self._here(stream)), "mla_add_norm_q8")
+        return codes, scales, residual_out, y
+
+    def quantize_rows(self, x: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                      scales: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """int8 codes of the rows of x [rows, d] (bf16 or fp32) and a scale for each: the input of
+        linear_q8, or its weight (x [n, k], a scale per output channel)."""
+        rows, d = x.shape if x.dim() == 2 else (-1, -1)
+        x_stride = self._rows(x, "x", ROW_TYPES)
+        codes, codes_stride, scales = self._new_codes(rows, d, codes, scales, x)
+        if rows > 0:
+            _check(self._lib.mla_quantize_rows(
+                self._h, rows, d, x.data_ptr(), ROW_TYPES[x.dtype], x_stride, codes.data_ptr(), codes_stride,
+                scales.data_ptr(), self._here(stream)), "mla_quantize_rows")
+        return codes, scales
+
+    def linear_q8(self, codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                  out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+        """out[i, j] = (codes[i] . w_codes[j]) * w_scales[j] * scales[i]: codes [rows, k] and
+        w_codes [n, k] int8, rows 16-byte aligned; scales [rows], w_scales [n] fp32. out [rows, n]
+        bf16 or fp32 (out_dtype unless given)."""
+        rows, k = codes.shape if codes.dim() == 2 else (-1, -1)
+        a_stride = self._rows(codes, "codes", (torch.int8,))
+        n = w_codes.shape[0]
+        w_stride = self._rows(w_codes, "w_codes", (torch.int8,), (n, k))
+        self._flat(scales, "scales", torch.float32, rows)
+        self._flat(w_scales, "w_scales", torch.float32, n)
+        if out is None:
+            out = torch.empty((rows, n), dtype=out_dtype, device=codes.device)
+        out_stride = self._rows(out, "out", ROW_TYPES, (rows, n))
+        if rows > 0:
+            _check(self._lib.mla_linear_q8(
+                self._h, rows, k, n, codes.data_ptr(), self._code_stride(codes, a_stride), scales.data_ptr(),
+                w_codes.data_ptr(), self._code_stride(w_codes, w_stride), w_scales.data_ptr(), out.data_ptr(),
+                ROW_TYPES[out.dtype], out_stride, self._here(stream)), "mla_linear_q8")
+        return out
+
+    def _append_rows_args(self, x, gamma, cache, cache_type, kv_lens, row_starts, page_table):
+        """The checked arguments that append_rows and append_rows_fp8 share."""
+        x_stride = self._rows(x, "x", ROW_TYPES)
+        if x.shape[1] != ROW:
+            raise ValueError(f"x: expected [rows, {ROW}], got {_shape(x)}")
+        self._flat(gamma, "gamma", torch.bfloat16, D_LATENT)
+        B = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+        self._flat(kv_lens, "kv_lens", torch.int32, B)
+        if row_starts is not None:
+            self._flat(row_starts, "row_starts", torch.int32, B + 1)
+        if cache.device != x.device or cache.dtype != cache_type or cache.dim() != 3 or cache.shape[2] != ROW or \
+                cache.stride(2) != 1 or cache.stride(1) < ROW:
+            raise ValueError(f"cache: expected {cache_type} [*, *, {ROW}] with unit inner stride on "
+                             f"cuda:{self.device}, got {_shape(cache)}")
+        row_stride = cache.stride(1)
+        seq_stride, rest = divmod(cache.stride(0), row_stride)
+        max_pages = num_pages = 0
+        if page_table is None:
+            if cache.shape[0] < B or (cache.shape[0] > 1 and (rest != 0 or seq_stride < cache.shape[1])) or \
+                    cache.shape[1] < self.cfg.max_kv_len:
+                raise ValueError(f"cache: expected [>= {B}, >= {self.cfg.max_kv_len}, {ROW}] with a whole number of "
+                                 f"rows between sequences, got {_shape(cache)}")
+            seq_stride = max(seq_stride, cache.shape[1])
+        else:
+            if page_table.device != x.device or page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+                    page_table.shape[0] < B or not page_table.is_contiguous():
+                raise ValueError(f"page_table: expected a contiguous int32 [>= {B}, pages] tensor on "
+                                 f"cuda:{self.device}, got {_shape(page_table)}")
+            if cache.shape[1] != self.cfg.page_size or (
+                    cache.shape[0] > 1 and cache.stride(0) != cache.shape[1] * row_stride):
+                raise ValueError(f"cache: expected pages of {self.cfg.page_size} rows end to end, got {_shape(cache)}")
+            max_pages, num_pages, seq_stride = page_table.shape[1], cache.shape[0], 0
+        return B, x_stride, row_stride, seq_stride, max_pages, num_pages
+
+    def append_rows(self, x: torch.Tensor, gamma: torch.Tensor, cache: torch.Tensor, kv_lens: torch.Tensor,
+                    row_starts: Optional[torch.Tensor] = None, page_table: Optional[torch.Tensor] = None,
+                    eps: float = 1e-6, stream=None) -> torch.Tensor:
+        """Write the cache rows [RMSNorm(x[:, :512])*gamma ; RoPE(x[:, 512:])] of projected rows x
+        [rows, 576] (bf16 or fp32; rows may lie apart): rows row_starts[b] .. row_starts[b+1]-1 are
+        the last of sequence b's kv_lens[b] tokens; without row_starts every sequence has q_len.
+        Rows outside every sequence write nothing. cache as for decode_attn; returned."""
+        B, x_stride, row_stride, seq_stride, max_pages, num_pages = self._append_rows_args(
+            x, gamma, cache, torch.bfloat16, kv_lens, row_starts, page_table)
+        c_kv = cache.data_ptr()
+        if x.shape[0] > 0:
+            _check(self._lib.mla_append_rows(
+                self._h, B, x.shape[0], x.data_ptr(), ROW_TYPES[x.dtype], x_stride, gamma.data_ptr(), eps, c_kv,
+                c_kv + 2 * D_LATENT, row_stride, seq_stride, kv_lens.data_ptr(),
+                None if row_starts is None else row_starts.data_ptr(),
+                None if page_table is None else page_table.data_ptr(), max_pages, num_pages, self._here(stream)),
+                "mla_append_rows")
+        return cache
+
+    def append_rows_fp8(self, x: torch.Tensor, gamma: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
+                        kv_lens: torch.Tensor, row_starts: Optional[torch.Tensor] = None,
+                        page_table: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None):
+        """append_rows into a quantised cache: codes uint8 and exps int8 as for decode_attn_fp8."""
+        B, x_stride, row_stride, seq_stride, max_pages, num_pages = self._append_rows_args(
+            x, gamma, codes, torch.uint8, kv_lens, row_starts, page_table)
+        if exps.device != x.device or exps.dtype != torch.int8 or exps.shape != codes.shape[:2] or \
+                not exps.is_contiguous() or (page_table is None and seq_stride != codes.shape[1]):
+            raise ValueError(f"exps: expected a contiguous int8 {tuple(codes.shape[:2])} tensor indexed as codes is, "
+                             f"got {_shape(exps)}")
+        if x.shape[0] > 0:
+            _check(self._lib.mla_append_rows_fp8(
+                self._h, B, x.shape[0], x.data_ptr(), ROW_TYPES[x.dtype], x_stride, gamma.data_ptr(), eps,
+                codes.data_ptr(), exps.data_ptr(), row_stride, seq_stride, kv_lens.data_ptr(),
+                None if row_starts is None else row_starts.data_ptr(),
+                None if page_table is None else page_table.data_ptr(), max_pages, num_pages, self._here(stream)),
+                "mla_append_rows_fp8")
+        return codes, exps
 
     def step(self, q_c, q_r, w_uk, w_uv, cache, kv_lens, page_table=None, stream=None,
              bufs: Optional[dict] = None):

@@ -20,6 +20,10 @@ constexpr int kMaxRows = 1 << 20;   // attention rows per sequence (heads x new 
 constexpr int kMaxTokenRows = 8192;  // (sequence, new token) rows per call: max_batch x new tokens
 constexpr int kMaxBatch = 1024;
 constexpr int kTileTokens = 64;  // tokens per KV tile: the unit of the work plan
+constexpr int kMaxNormWidth = 16384;      // add_norm_q8, quantize_rows: 16 values per thread of a block
+constexpr int kMaxLinearK = 131071;       // linear_q8: |sum| <= 2^14 k stays below 2^31
+constexpr int kMaxLinearRows = 1 << 20;   // ... rows and output channels
+constexpr int64_t kMaxLinearStride = (int64_t)1 << 32;   // ... bytes between rows (below TMA's 2^40)
 constexpr int kAppendSlices = 16;  // the cache write's projection is split over at most 16 slices of d
 
 // Device error word bits (see mla_check_device_errors).
@@ -102,6 +106,27 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// The same with the grid's x cut into clusters of `cluster` blocks.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                      int cluster, cudaStream_t s, Args&&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // Launchers (each returns the cudaGetLastError() of its launch).
 cudaError_t launch_absorb_q(const mla_decode_s& h, int batch, const __nv_bfloat16* q_c,
                             const __nv_bfloat16* q_r, const __nv_bfloat16* w_uk,
@@ -170,5 +195,47 @@ cudaError_t launch_absorb_q_fp8(const mla_decode_s& h, int batch, const __nv_bfl
 cudaError_t launch_apply_wuv_fp8(const mla_decode_s& h, int batch, const __nv_bfloat16* latent,
                                  const uint8_t* w_uv_codes, const int8_t* w_uv_exp,
                                  __nv_bfloat16* out, cudaStream_t s);
+
+// Rows into int8 codes with a scale each (gamma == nullptr: no norm). Strides in elements.
+struct NormArgs {
+  int64_t n_rows;
+  int d;
+  const void* x;
+  bool x_f32;
+  int64_t x_stride;
+  const void* residual;   // nullptr: none
+  void* residual_out;
+  bool residual_f32;
+  int64_t residual_stride, residual_out_stride;
+  const __nv_bfloat16* gamma;
+  float eps;
+  __nv_bfloat16* y;       // nullptr: not wanted
+  int64_t y_stride;
+  int8_t* codes;          // nullptr: not wanted
+  int64_t codes_stride;
+  float* scales;
+};
+cudaError_t launch_norm_q8(const NormArgs& a, cudaStream_t s);
+
+// out [rows, n] = (codes [rows, k] . w_codes [n, k]) scaled per row and per column.
+struct LinearArgs {
+  int rows, n, k;
+  const int8_t* codes;
+  int64_t codes_stride;
+  const float* scales;
+  const int8_t* w_codes;
+  int64_t w_stride;
+  const float* w_scales;
+  void* out;
+  bool out_f32;
+  int64_t out_stride;
+};
+cudaError_t launch_linear_q8(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s);
+
+// The cache rows of n_rows projected rows x [n_rows, 576] (cv.kv_exp != nullptr: E4M3 codes at c_kv).
+cudaError_t launch_append_rows(const mla_decode_s& h, int batch, int n_rows, const void* x, bool x_f32,
+                               int64_t x_stride, const __nv_bfloat16* gamma, float eps, const CacheView& cv,
+                               __nv_bfloat16* c_kv, __nv_bfloat16* k_r, const int32_t* kv_lens,
+                               const int32_t* row_starts, cudaStream_t s);
 
 }  // namespace mla

@@ -340,8 +340,8 @@ enum {
  * Residual addition, RMSNorm and int8 quantisation with one scale per row:
  *   r      = x + residual (fp32; r = x without one);  residual_out = r in the residual's type
  *   rstd   = 1 / sqrt(mean(r^2) + rms_eps)
- *   y      = r * rstd * gamma                                                      (bf16)
- *   codes  = the integers nearest to 127 t / m, ties to even, t = r * gamma (fp32), m = max|t|
+ *   t      = r * gamma (fp32);  y = t * rstd                                       (bf16)
+ *   codes  = the integers nearest to 127 t / m, ties to even, m = max|t|
  *   scales = m * rstd / 127, so that codes * scales is the normalised row to half a code
  * A row of zeros gets codes 0 and scale 0; a row with an infinity or a NaN in t gets codes 0 and a
  * NaN scale. Codes depend on no sum: they are the same on every run and for any layout.
@@ -353,8 +353,8 @@ enum {
  * y             bf16 [n_rows, d], or NULL: not wanted; may be x itself where x is bf16
  * codes, scales int8 [n_rows, d] and fp32 [n_rows], or both NULL: not wanted (y is wanted then).
  *               mla_linear_q8 reads codes that are 16-byte aligned, rows a multiple of 16 apart.
- * Rows that are 16-byte aligned everywhere (codes 8-byte) with d a multiple of 8 are moved 16
- * bytes at a time.
+ * Fastest where d is a multiple of 8 and all rows are 16-byte aligned (codes 8-byte); 4, 2 or 1
+ * values at a time else.
  * Errors: MLA_ERR_INVALID_ARG for NULL pointers, a bad type, size, stride, rms_eps or alignment;
  * MLA_ERR_UNSUPPORTED for d > 16384 or n_rows >= 2^31.
  */

@@ -30,6 +30,7 @@ ROW = 576
 D_LATENT = 512
 
 ROW_TYPES = {torch.bfloat16: 0, torch.float32: 1}   # MLA_BF16, MLA_F32
+_INT8 = (torch.int8,)
 
 
 class MlaConfig(ctypes.Structure):
@@ -459,37 +460,36 @@ class MlaDecode:
 
     def _rows(self, t: torch.Tensor, name: str, dtypes, shape=None) -> int:
         """The stride between the rows of a [rows, d] tensor on the handle's device."""
-        if t.device.type != "cuda" or t.device.index != self.device or t.dtype not in dtypes or t.dim() != 2 or \
-                (t.shape[1] > 1 and t.stride(1) != 1) or (shape is not None and t.shape != shape):
-            raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dtypes)} "
-                             f"{'[rows, d]' if shape is None else tuple(shape)} with unit inner stride "
-                             f"on cuda:{self.device}, got {_shape(t)}")
-        stride = t.stride(0)
-        if t.shape[0] > 1 and stride < t.shape[1]:
-            raise ValueError(f"{name}: rows overlap, got {_shape(t)}")
-        return stride if t.shape[0] > 1 and stride > t.shape[1] else t.shape[1]
+        sizes, strides = t.shape, t.stride()
+        if len(strides) == 2 and t.dtype in dtypes and t.get_device() == self.device and \
+                (shape is None or sizes == shape):
+            rows, d = sizes
+            if strides[1] == 1 or d <= 1:
+                if rows <= 1:
+                    return d
+                if strides[0] >= d:
+                    return strides[0]
+        raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dtypes)} "
+                         f"{'[rows, d]' if shape is None else tuple(shape)} with unit inner stride and rows "
+                         f"apart on cuda:{self.device}, got {_shape(t)}")
 
     def _flat(self, t: torch.Tensor, name: str, dtype, n: int) -> None:
-        if t.device.type != "cuda" or t.device.index != self.device or t.dtype != dtype or t.dim() != 1 or \
-                t.shape[0] != n or not t.is_contiguous():
+        if t.dtype != dtype or t.get_device() != self.device or t.shape != (n,) or not t.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous {dtype} [{n}] tensor on cuda:{self.device}, "
                              f"got {_shape(t)}")
 
-    def _new_codes(self, rows: int, d: int, codes, scales, x):
+    def _new_codes(self, rows: int, d: int, codes, scales, device):
         """Codes and scales to write (rows of new codes are a multiple of 16 bytes apart)."""
         if codes is None:
-            codes = torch.empty((rows, (d + 15) // 16 * 16), dtype=torch.int8, device=x.device)
-            codes = codes if d % 16 == 0 else codes[:, :d]
+            stride = (d + 15) // 16 * 16
+            codes = torch.empty_strided((rows, d), (stride, 1), dtype=torch.int8, device=device)
+        else:
+            stride = self._rows(codes, "codes", _INT8, (rows, d))
         if scales is None:
-            scales = torch.empty(rows, dtype=torch.float32, device=x.device)
-        stride = self._rows(codes, "codes", (torch.int8,), (rows, d))
-        self._flat(scales, "scales", torch.float32, rows)
+            scales = torch.empty_strided((rows,), (1,), dtype=torch.float32, device=device)
+        else:
+            self._flat(scales, "scales", torch.float32, rows)
         return codes, stride, scales
-
-    @staticmethod
-    def _code_stride(t: torch.Tensor, stride: int) -> int:
-        """One row of codes has no stride of its own: any multiple of 16 will do."""
-        return stride if t.shape[0] > 1 else (stride + 15) // 16 * 16
 
     def add_norm_q8(self, x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None,
                     eps: float = 1e-6, want_y: bool = False, residual_out: Optional[torch.Tensor] = None,
@@ -500,23 +500,26 @@ class MlaDecode:
         bf16. Returns (codes int8 [rows, d], scales fp32 [rows], residual_out, y): residual_out is
         r in the residual's type (a new tensor unless given; `residual` itself is allowed), None
         without a residual; y is the normalised row in bf16, None unless wanted or given."""
-        rows, d = x.shape if x.dim() == 2 else (-1, -1)
         x_stride = self._rows(x, "x", ROW_TYPES)
+        rows, d = shape = x.shape
+        device = x.device
         self._flat(gamma, "gamma", torch.bfloat16, d)
         res_stride = out_stride = y_stride = res_type = 0
         if residual is not None:
-            res_stride = self._rows(residual, "residual", ROW_TYPES, x.shape)
+            res_stride = self._rows(residual, "residual", ROW_TYPES, shape)
             if residual_out is None:
-                residual_out = torch.empty((rows, d), dtype=residual.dtype, device=x.device)
-            out_stride = self._rows(residual_out, "residual_out", (residual.dtype,), x.shape)
+                residual_out = torch.empty_strided(shape, (d, 1), dtype=residual.dtype, device=device)
+                out_stride = d
+            else:
+                out_stride = self._rows(residual_out, "residual_out", (residual.dtype,), shape)
             res_type = ROW_TYPES[residual.dtype]
         elif residual_out is not None:
             raise ValueError("residual_out without a residual")
-        codes, codes_stride, scales = self._new_codes(rows, d, codes, scales, x)
-        if y is None and want_y:
-            y = torch.empty((rows, d), dtype=torch.bfloat16, device=x.device)
+        codes, codes_stride, scales = self._new_codes(rows, d, codes, scales, device)
         if y is not None:
-            y_stride = self._rows(y, "y", (torch.bfloat16,), x.shape)
+            y_stride = self._rows(y, "y", (torch.bfloat16,), shape)
+        elif want_y:
+            y, y_stride = torch.empty_strided(shape, (d, 1), dtype=torch.bfloat16, device=device), d
         if rows > 0:
             _check(self._lib.mla_add_norm_q8(
                 self._h, rows, d, x.data_ptr(), ROW_TYPES[x.dtype], x_stride,
@@ -530,9 +533,9 @@ class MlaDecode:
                       scales: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """int8 codes of the rows of x [rows, d] (bf16 or fp32) and a scale for each: the input of
         linear_q8, or its weight (x [n, k], a scale per output channel)."""
-        rows, d = x.shape if x.dim() == 2 else (-1, -1)
         x_stride = self._rows(x, "x", ROW_TYPES)
-        codes, codes_stride, scales = self._new_codes(rows, d, codes, scales, x)
+        rows, d = x.shape
+        codes, codes_stride, scales = self._new_codes(rows, d, codes, scales, x.device)
         if rows > 0:
             _check(self._lib.mla_quantize_rows(
                 self._h, rows, d, x.data_ptr(), ROW_TYPES[x.dtype], x_stride, codes.data_ptr(), codes_stride,
@@ -544,20 +547,31 @@ class MlaDecode:
         """out[i, j] = (codes[i] . w_codes[j]) * w_scales[j] * scales[i]: codes [rows, k] and
         w_codes [n, k] int8, rows 16-byte aligned; scales [rows], w_scales [n] fp32. out [rows, n]
         bf16 or fp32 (out_dtype unless given)."""
-        rows, k = codes.shape if codes.dim() == 2 else (-1, -1)
-        a_stride = self._rows(codes, "codes", (torch.int8,))
-        n = w_codes.shape[0]
-        w_stride = self._rows(w_codes, "w_codes", (torch.int8,), (n, k))
+        a_stride = self._rows(codes, "codes", _INT8)
+        rows, k = codes.shape
+        w_stride = self._rows(w_codes, "w_codes", _INT8)
+        n, w_k = w_codes.shape
+        if w_k != k:
+            raise ValueError(f"w_codes: expected [n, {k}], got {_shape(w_codes)}")
         self._flat(scales, "scales", torch.float32, rows)
         self._flat(w_scales, "w_scales", torch.float32, n)
-        if out is None:
-            out = torch.empty((rows, n), dtype=out_dtype, device=codes.device)
-        out_stride = self._rows(out, "out", ROW_TYPES, (rows, n))
+        if out is not None:
+            out_dtype = out.dtype
+            out_stride = self._rows(out, "out", ROW_TYPES, (rows, n))
+        else:
+            if out_dtype not in ROW_TYPES:
+                raise ValueError(f"out_dtype: expected torch.bfloat16 or torch.float32, got {out_dtype}")
+            out, out_stride = torch.empty_strided((rows, n), (n, 1), dtype=out_dtype, device=codes.device), n
+        # one row has no stride of its own: any multiple of 16 will do
+        if rows == 1:
+            a_stride = (k + 15) // 16 * 16
+        if n == 1:
+            w_stride = (k + 15) // 16 * 16
         if rows > 0:
             _check(self._lib.mla_linear_q8(
-                self._h, rows, k, n, codes.data_ptr(), self._code_stride(codes, a_stride), scales.data_ptr(),
-                w_codes.data_ptr(), self._code_stride(w_codes, w_stride), w_scales.data_ptr(), out.data_ptr(),
-                ROW_TYPES[out.dtype], out_stride, self._here(stream)), "mla_linear_q8")
+                self._h, rows, k, n, codes.data_ptr(), a_stride, scales.data_ptr(), w_codes.data_ptr(), w_stride,
+                w_scales.data_ptr(), out.data_ptr(), ROW_TYPES[out_dtype], out_stride, self._here(stream)),
+                "mla_linear_q8")
         return out
 
     def _append_rows_args(self, x, gamma, cache, cache_type, kv_lens, row_starts, page_table):
@@ -570,29 +584,26 @@ class MlaDecode:
         self._flat(kv_lens, "kv_lens", torch.int32, B)
         if row_starts is not None:
             self._flat(row_starts, "row_starts", torch.int32, B + 1)
-        if cache.device != x.device or cache.dtype != cache_type or cache.dim() != 3 or cache.shape[2] != ROW or \
-                cache.stride(2) != 1 or cache.stride(1) < ROW:
+        sizes, strides = cache.shape, cache.stride()
+        if cache.get_device() != self.device or cache.dtype != cache_type or len(sizes) != 3 or \
+                sizes[2] != ROW or strides[2] != 1 or strides[1] < ROW:
             raise ValueError(f"cache: expected {cache_type} [*, *, {ROW}] with unit inner stride on "
                              f"cuda:{self.device}, got {_shape(cache)}")
-        row_stride = cache.stride(1)
-        seq_stride, rest = divmod(cache.stride(0), row_stride)
-        max_pages = num_pages = 0
+        row_stride = strides[1]
         if page_table is None:
-            if cache.shape[0] < B or (cache.shape[0] > 1 and (rest != 0 or seq_stride < cache.shape[1])) or \
-                    cache.shape[1] < self.cfg.max_kv_len:
+            seq_stride, rest = divmod(strides[0], row_stride)
+            if sizes[0] < B or (sizes[0] > 1 and (rest != 0 or seq_stride < sizes[1])) or \
+                    sizes[1] < self.cfg.max_kv_len:
                 raise ValueError(f"cache: expected [>= {B}, >= {self.cfg.max_kv_len}, {ROW}] with a whole number of "
                                  f"rows between sequences, got {_shape(cache)}")
-            seq_stride = max(seq_stride, cache.shape[1])
-        else:
-            if page_table.device != x.device or page_table.dtype != torch.int32 or page_table.dim() != 2 or \
-                    page_table.shape[0] < B or not page_table.is_contiguous():
-                raise ValueError(f"page_table: expected a contiguous int32 [>= {B}, pages] tensor on "
-                                 f"cuda:{self.device}, got {_shape(page_table)}")
-            if cache.shape[1] != self.cfg.page_size or (
-                    cache.shape[0] > 1 and cache.stride(0) != cache.shape[1] * row_stride):
-                raise ValueError(f"cache: expected pages of {self.cfg.page_size} rows end to end, got {_shape(cache)}")
-            max_pages, num_pages, seq_stride = page_table.shape[1], cache.shape[0], 0
-        return B, x_stride, row_stride, seq_stride, max_pages, num_pages
+            return B, x_stride, row_stride, max(seq_stride, sizes[1]), 0, 0
+        if page_table.get_device() != self.device or page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+                page_table.shape[0] < B or not page_table.is_contiguous():
+            raise ValueError(f"page_table: expected a contiguous int32 [>= {B}, pages] tensor on "
+                             f"cuda:{self.device}, got {_shape(page_table)}")
+        if sizes[1] != self.cfg.page_size or (sizes[0] > 1 and strides[0] != sizes[1] * row_stride):
+            raise ValueError(f"cache: expected pages of {self.cfg.page_size} rows end to end, got {_shape(cache)}")
+        return B, x_stride, row_stride, 0, page_table.shape[1], sizes[0]
 
     def append_rows(self, x: torch.Tensor, gamma: torch.Tensor, cache: torch.Tensor, kv_lens: torch.Tensor,
                     row_starts: Optional[torch.Tensor] = None, page_table: Optional[torch.Tensor] = None,
@@ -619,7 +630,7 @@ class MlaDecode:
         """append_rows into a quantised cache: codes uint8 and exps int8 as for decode_attn_fp8."""
         B, x_stride, row_stride, seq_stride, max_pages, num_pages = self._append_rows_args(
             x, gamma, codes, torch.uint8, kv_lens, row_starts, page_table)
-        if exps.device != x.device or exps.dtype != torch.int8 or exps.shape != codes.shape[:2] or \
+        if exps.get_device() != self.device or exps.dtype != torch.int8 or exps.shape != codes.shape[:2] or \
                 not exps.is_contiguous() or (page_table is None and seq_stride != codes.shape[1]):
             raise ValueError(f"exps: expected a contiguous int8 {tuple(codes.shape[:2])} tensor indexed as codes is, "
                              f"got {_shape(exps)}")

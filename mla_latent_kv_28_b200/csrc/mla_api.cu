@@ -523,7 +523,7 @@ int rows_q8_common(mla_handle_t h, const mla::NormArgs& a, int32_t x_type, int32
   if (a.n_rows == 0) return MLA_OK;
   const OnDevice on(h->device);
   if (!on.ok()) return MLA_ERR_CUDA;
-  return mla::launch_norm_q8(a, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return mla::launch_norm_q8(*h, a, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 // The shared body of mla_append_rows (bf16 rows) and mla_append_rows_fp8 (kv_exp != nullptr:

@@ -215,7 +215,7 @@ struct NormArgs {
   int64_t codes_stride;
   float* scales;
 };
-cudaError_t launch_norm_q8(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_q8(const mla_decode_s& h, const NormArgs& a, cudaStream_t s);
 
 // out [rows, n] = (codes [rows, k] . w_codes [n, k]) scaled per row and per column.
 struct LinearArgs {

@@ -1,32 +1,41 @@
 // Rows on their way into an int8 product:
 //
 //   add_norm_q8     r = x + residual (fp32), residual_out = r in the residual's type
-//                   y = r / sqrt(mean(r^2) + eps) * gamma                          (bf16)
+//                   t = r * gamma (fp32), rstd = 1 / sqrt(mean(r^2) + eps), y = t * rstd (bf16)
 //                   codes, scale with code * scale = y to half a code
-//   quantize_rows   codes, scale of x itself
+//   quantize_rows   codes, scale of t = x itself, rstd = 1
 //
-// The row's own factor rstd = 1/sqrt(mean(r^2) + eps) is common to all its values, so it cancels
-// from the codes: with t = r * gamma and m = max|t|, code = round(127 t / m) and
-// scale = m rstd / 127. The sum of squares and the maximum are therefore taken in one reduction
-// over values that stay in registers (one pass over memory), and the codes depend on no sum:
-// they are the exact nearest integers (ties to even) of 127 t / m for the fp32 t and m, the same
-// on every run and for every block size. The quotient is first taken in fp32 (its error is under
-// 127 * 4 * 2^-24 = 3.1e-5); only a value within 1e-4 of a border between two codes is decided
-// again by comparing 127 t with (j + 1/2) m, both exact in fp64 (24 + 8 bits each).
+// rstd is common to a row's values, so it cancels from the codes: with m = max|t|,
+// code = round(127 t / m) and scale = m rstd / 127. The sum of squares and the maximum are therefore
+// taken in one reduction over values that stay in registers (one pass over memory), and the codes
+// depend on no sum: they are the nearest integers (ties to even) of 127 t / m for the fp32 t and m,
+// the same on every run and for every layout. The integer is first taken from t * (127 / m) in fp32,
+// off by the reciprocal's rounding, under 127 * 2^-24 = 7.6e-6; where the distance to it exceeds
+// 0.49998 the eight values are taken again from 127 t / m in fp64 (a quotient of a 31-bit by a
+// 24-bit number that is not on a border lies at least 2^-33 off it).
 //
-// One block per row; a thread holds NV vectors of 8 neighbouring values (or, for rows that are
-// not 16-byte aligned, 16 values a block apart). Bound by HBM: per value the bytes of x, the
-// residual in and out, one code, and y where it is wanted.
+// A group of threads takes a row: 8, 16 or 32 lanes up to 1024 values, a block of its own beyond. A
+// thread holds NV vectors of 8 values of t (neighbours where rows are 16-byte aligned) and nothing
+// else across the reduction. Bound by HBM: per value the bytes of x, the residual in and out, one
+// code, and y where it is wanted; then by the issue slots (packed fp32 pairs and three-way maxima:
+// some 5 instructions per value without a norm). Measured: 4096 x 5120 bf16 with an fp32 residual
+// and y 42.5 us (6420 GB/s); 2048 x 16384 bf16 quantised 22.6 us (4450 GB/s, the codes' instructions
+// and the two phases of a row not fully hidden); one row of 5120 2.2 us, the launch and one round trip.
+// Rows of odd width (one value at a time) run at half to three quarters of that.
 #include <algorithm>
 #include <type_traits>
 
 #include "mla_internal.cuh"
 #include "rows.cuh"
+#include "sm100.cuh"
 
 namespace mla {
 namespace {
 
+constexpr int kGroupThreads = 256;   // threads of a block whose lanes take a row in groups
+
 struct NormParams {
+  int64_t n_rows;
   const void* x;
   const void* res;        // nullptr: none
   void* res_out;
@@ -41,203 +50,392 @@ struct NormParams {
 
 struct NoResidual {};
 
-// The low byte is the code: the integer nearest to 127 t / m (ties to even), with inv = 127 / m.
-__device__ __forceinline__ uint32_t code_of(float t, float m, float inv) {
-  constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer
-  const float v = t * inv;
-  float k = v + kMagic;
-  if (fabsf(v - (k - kMagic)) > 0.4999f) {
-    const double j = floor((double)v);   // the border is j + 1/2: fp32's v is within 1e-4 of it
-    const double a = (double)t * 127.0, c = (double)m * (j + 0.5);
-    const bool up = a > c || (a == c && fmod(j, 2.0) != 0.0);
-    k = (float)(j + (up ? 1.0 : 0.0)) + kMagic;
-  }
-  return __float_as_uint(k);
+// max(a, |b|, |c|), and NaN if one of them is
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
-// RT: the residual's type, or NoResidual. kVec: every row's pointers are aligned for 8 values at
-// a time and d is a multiple of 8; value i of thread `tid`, vector n, is 8 (n blockDim + tid) + i,
-// otherwise (8 n + i) blockDim + tid.
-template <typename XT, typename RT, bool kNorm, int NV, bool kVec>
-__global__ void __launch_bounds__(1024)
-norm_q8_kernel(const NormParams p) {
-  constexpr bool kRes = !std::is_same<RT, NoResidual>::value;
-  __shared__ float part_ss[32];
-  __shared__ uint32_t part_m[32];
-  __shared__ double part_d[32];
-  const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31, warps = nthr >> 5;
-  const int64_t row = blockIdx.x;
-  const XT* x = static_cast<const XT*>(p.x) + row * p.x_stride;
-  grid_dependency_wait();
-  allow_dependent_launch();
+// Eight values as loaded, in pairs: W neighbouring ones at p, W more at p + step, and so on while
+// they lie before `left` values from p.
+template <typename T, int W>
+struct Raw8;
+template <int W>
+struct Raw8<__nv_bfloat16, W> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int step, int left) {
+#pragma unroll
+    for (int c = 0; c < 8 / W; ++c) {
+      const __nv_bfloat16* q = p + (int64_t)c * step;
+      const bool in = c * step < left;
+      if constexpr (W == 8) {
+        const uint4 u = in ? *reinterpret_cast<const uint4*>(q) : make_uint4(0, 0, 0, 0);
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+      } else if constexpr (W == 4) {
+        const uint2 u = in ? *reinterpret_cast<const uint2*>(q) : make_uint2(0, 0);
+        w[2 * c] = u.x; w[2 * c + 1] = u.y;
+      } else if constexpr (W == 2) {
+        w[c] = in ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+      } else {
+        const uint32_t u = in ? *reinterpret_cast<const uint16_t*>(q) : 0u;
+        w[c >> 1] = c & 1 ? w[c >> 1] | u << 16 : u;
+      }
+    }
+  }
+  __device__ __forceinline__ float2 pair(int i) const {
+    return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+};
+template <int W>
+struct Raw8<float, W> {
+  float2 v[4];
+  __device__ __forceinline__ void load(const float* p, int step, int left) {
+#pragma unroll
+    for (int c = 0; c < 8 / W; ++c) {
+      const float* q = p + (int64_t)c * step;
+      const bool in = c * step < left;
+      if constexpr (W >= 4) {
+#pragma unroll
+        for (int h = 0; h < W / 4; ++h) {
+          const float4 a = in ? reinterpret_cast<const float4*>(q)[h] : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[c * W / 2 + 2 * h] = make_float2(a.x, a.y);
+          v[c * W / 2 + 2 * h + 1] = make_float2(a.z, a.w);
+        }
+      } else if constexpr (W == 2) {
+        v[c] = in ? *reinterpret_cast<const float2*>(q) : make_float2(0.f, 0.f);
+      } else {
+        const float a = in ? *q : 0.f;
+        if (c & 1) v[c >> 1].y = a;
+        else v[c >> 1].x = a;
+      }
+    }
+  }
+  __device__ __forceinline__ float2 pair(int i) const { return v[i]; }
+};
 
-  float r[NV][8], g[NV][8];
+template <int W>
+__device__ __forceinline__ void store_pairs(float* p, int step, int left, const float2 (&v)[4]) {
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    if constexpr (kVec) {
-      const int e = 8 * (n * nthr + tid);
-      const bool in = e < p.d;
+  for (int c = 0; c < 8 / W; ++c) {
+    if (c * step >= left) continue;
+    float* q = p + (int64_t)c * step;
+    if constexpr (W >= 4) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r[n][i] = 0.f, g[n][i] = 0.f;
-      if (in) load8(x + e, r[n]);
-      if constexpr (kNorm)
-        if (in) load8(p.gamma + e, g[n]);
+      for (int h = 0; h < W / 4; ++h) {
+        const float2 a = v[c * W / 2 + 2 * h], b = v[c * W / 2 + 2 * h + 1];
+        reinterpret_cast<float4*>(q)[h] = make_float4(a.x, a.y, b.x, b.y);
+      }
+    } else if constexpr (W == 2) {
+      *reinterpret_cast<float2*>(q) = v[c];
+    } else {
+      *q = c & 1 ? v[c >> 1].y : v[c >> 1].x;
+    }
+  }
+}
+template <int W>
+__device__ __forceinline__ void store_pairs(__nv_bfloat16* p, int step, int left, const float2 (&v)[4]) {
+#pragma unroll
+  for (int c = 0; c < 8 / W; ++c) {
+    if (c * step >= left) continue;
+    __nv_bfloat16* q = p + (int64_t)c * step;
+    if constexpr (W == 8)
+      *reinterpret_cast<uint4*>(q) = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
+                                                pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
+    else if constexpr (W == 4)
+      *reinterpret_cast<uint2*>(q) = make_uint2(pack_bf16(v[2 * c].x, v[2 * c].y), pack_bf16(v[2 * c + 1].x, v[2 * c + 1].y));
+    else if constexpr (W == 2)
+      *reinterpret_cast<uint32_t*>(q) = pack_bf16(v[c].x, v[c].y);
+    else
+      *q = __float2bfloat16_rn(c & 1 ? v[c >> 1].y : v[c >> 1].x);
+  }
+}
+template <int W>
+__device__ __forceinline__ void store_codes(int8_t* p, int step, int left, uint2 v) {
+#pragma unroll
+  for (int c = 0; c < 8 / W; ++c) {
+    if (c * step >= left) continue;
+    int8_t* q = p + (int64_t)c * step;
+    if constexpr (W == 8) *reinterpret_cast<uint2*>(q) = v;
+    else if constexpr (W == 4) *reinterpret_cast<uint32_t*>(q) = c ? v.y : v.x;
+    else if constexpr (W == 2) *reinterpret_cast<uint16_t*>(q) = (uint16_t)((c & 2 ? v.y : v.x) >> (16 * (c & 1)));
+    else *q = (int8_t)((c & 4 ? v.y : v.x) >> (8 * (c & 3)));
+  }
+}
+
+// A row's statistics so far. The squares of values over 1e15 or under 1e-13 go to an fp64 sum, so
+// that none of them leaves fp32's range and none is lost.
+struct Stats {
+  float ss = 0.f, m = 0.f;
+  double dd = 0.0;
+  __device__ __forceinline__ void squares(const float2 (&r)[4]) {
+    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s2 = sm100::ffma2(r[i], r[i], s2);
+    const float s = s2.x + s2.y;
+    if (s > 1e-25f && s < 1e30f) {
+      ss += s;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = (8 * n + i) * nthr + tid;
-        r[n][i] = e < p.d ? load1(x + e) : 0.f;
-        if constexpr (kNorm) g[n][i] = e < p.d ? load1(p.gamma + e) : 0.f;
-      }
+      for (int i = 0; i < 4; ++i) dd = fma((double)r[i].x, (double)r[i].x, fma((double)r[i].y, (double)r[i].y, dd));
     }
   }
-  if constexpr (kRes) {
-    const RT* res = static_cast<const RT*>(p.res) + row * p.res_stride;
-    RT* out = static_cast<RT*>(p.res_out) + row * p.res_out_stride;
+  __device__ __forceinline__ void largest(const float2 (&t)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max_abs_nan(m, t[i].x, t[i].y);
+  }
+};
+
+// The integers nearest to 127 t / m, ties to even, the slow way.
+__device__ __noinline__ uint2 exact_codes(float2 a, float2 b, float2 c, float2 d, float m) {
+  const float t[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i >> 2] |= ((uint32_t)__double2int_rn((double)t[i] * 127.0 / (double)m) & 0xFFu) << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+
+// Eight codes; inv = 127 / m (0: a row of zeros).
+__device__ __forceinline__ uint2 codes8(const float2 (&t)[4], float m, float inv) {
+  constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer in the low bits
+  const float2 inv2 = make_float2(inv, inv), magic = make_float2(kMagic, kMagic);
+  float2 k[4];
+  float off = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    k[i] = sm100::ffma2(t[i], inv2, magic);
+    const float2 j = sm100::fadd2(k[i], make_float2(-kMagic, -kMagic));
+    const float2 e = sm100::ffma2(t[i], inv2, make_float2(-j.x, -j.y));
+    off = max_abs(off, e.x, e.y);
+  }
+  if (off > 0.49998f) return exact_codes(t[0], t[1], t[2], t[3], m);
+  const auto pack = [](const float2& a, const float2& b) {
+    return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                       __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+  };
+  return make_uint2(pack(k[0], k[1]), pack(k[2], k[3]));
+}
+
+// RT: the residual's type, or NoResidual. G: the lanes that share a row, or 0: a block per row. W:
+// the values that all rows' pointers are aligned for (d is a multiple). With nthr threads per row,
+// vector n of thread `tid` is 8/W pieces, piece c the W values from W ((8/W n + c) nthr + tid) on.
+template <typename XT, typename RT, bool kNorm, int NV, int W, int G>
+__global__ void __launch_bounds__(G > 0 ? kGroupThreads : NV > 2 ? 512 : 1024,
+                                  G > 0 ? 1 : NV > 2 ? (!kNorm && sizeof(XT) == 2 ? 3 : 2) : 1)
+norm_q8_kernel(const NormParams p) {
+  constexpr bool kRes = !std::is_same<RT, NoResidual>::value;
+  using Res = typename std::conditional<kRes, RT, float>::type;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = G > 0 ? (int)threadIdx.x % (G > 0 ? G : 1) : (int)threadIdx.x, nthr = G > 0 ? G : (int)blockDim.x;
+  int64_t row = blockIdx.x;
+  if (G > 0) row = row * (kGroupThreads / (G > 0 ? G : 1)) + threadIdx.x / (G > 0 ? G : 1);
+  grid_dependency_wait();
+  allow_dependent_launch();
+  // groups behind the last row take part in the warp's exchanges, with nothing to read or write
+  const int d = G == 0 || row < p.n_rows ? p.d : 0;
+  const XT* x = static_cast<const XT*>(p.x) + row * p.x_stride;
+  const Res* res = static_cast<const Res*>(p.res) + row * p.res_stride;
+  Res* res_out = static_cast<Res*>(p.res_out) + row * p.res_out_stride;
+  const int step = W * nthr;
+
+  // what stays in registers across the reduction: t, or x as loaded where that is t
+  float2 t[kNorm ? NV : 1][4];
+  Raw8<XT, W> rx[NV];
+  Stats st;
+  if constexpr (!kNorm) {
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      if constexpr (kVec) {
-        const int e = 8 * (n * nthr + tid);
-        if (e < p.d) {
-          float a[8];
-          load8(res + e, a);
+      const int e = W * (8 / W * n * nthr + tid);
+      rx[n].load(x + e, step, d - e);
+    }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) r[n][i] += a[i];
-          store8(out + e, r[n]);
-        }
-      } else {
+    for (int n = 0; n < NV; ++n) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = (8 * n + i) * nthr + tid;
-          if (e < p.d) {
-            r[n][i] += load1(res + e);
-            store1(out + e, r[n][i]);
-          }
-        }
+      for (int i = 0; i < 4; ++i) t[0][i] = rx[n].pair(i);
+      st.largest(t[0]);
+    }
+  } else {
+    Raw8<Res, W> rr[NV];
+    Raw8<__nv_bfloat16, W> rg[NV];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int e = W * (8 / W * n * nthr + tid);
+      rx[n].load(x + e, step, d - e);
+      if constexpr (kRes) rr[n].load(res + e, step, d - e);
+      rg[n].load(p.gamma + e, step, d - e);
+    }
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int e = W * (8 / W * n * nthr + tid);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        t[n][i] = rx[n].pair(i);
+        if constexpr (kRes) t[n][i] = sm100::fadd2(t[n][i], rr[n].pair(i));
+      }
+      if constexpr (kRes) store_pairs<W>(res_out + e, step, d - e, t[n]);
+      st.squares(t[n]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 g = rg[n].pair(i);
+        t[n][i] = make_float2(t[n][i].x * g.x, t[n][i].y * g.y);
+      }
+      st.largest(t[n]);
+    }
+  }
+
+  // the row's maximum and sum of squares
+  uint32_t mb = __float_as_uint(st.m);   // NaN above infinity above all
+  float ss = st.ss;
+  bool wide = st.dd != 0.0;   // NaN too
+  double dd = st.dd;
+  if constexpr (G > 0) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      wide = __any_sync(0xffffffffu, wide);
+      if (wide) {
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, o);
+      }
+    }
+  } else {
+    __shared__ float part_ss[32];
+    __shared__ uint32_t part_m[32];
+    const int warps = nthr >> 5;
+    mb = __reduce_max_sync(0xffffffffu, mb);
+    if constexpr (kNorm) ss = warp_sum(ss);
+    if (lane == 0) {
+      part_ss[warp] = ss;
+      part_m[warp] = mb;
+    }
+    if constexpr (kNorm) wide = __syncthreads_or(wide);
+    else __syncthreads();
+    mb = __reduce_max_sync(0xffffffffu, lane < warps ? part_m[lane] : 0u);
+    if constexpr (kNorm) {
+      ss = warp_sum(lane < warps ? part_ss[lane] : 0.f);
+      if (wide) {   // the same for the whole block
+        __shared__ double part_d[32];
+        dd = warp_sum(dd);
+        if (lane == 0) part_d[warp] = dd;
+        __syncthreads();
+        dd = warp_sum(lane < warps ? part_d[lane] : 0.0);
       }
     }
   }
-
-  // one reduction: the sum of squares, and the largest |t| as the bits of a float, an order in
-  // which infinity and NaN lie above every finite value
-  float ss = 0.f;
-  uint32_t mb = 0;
-#pragma unroll
-  for (int n = 0; n < NV; ++n)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (kNorm) ss = fmaf(r[n][i], r[n][i], ss);
-      const float t = kNorm ? r[n][i] * g[n][i] : r[n][i];
-      mb = max(mb, __float_as_uint(fabsf(t)));
-    }
-  if constexpr (kNorm) ss = warp_sum(ss);
-  mb = __reduce_max_sync(0xffffffffu, mb);
-  if (lane == 0) {
-    part_ss[warp] = ss;
-    part_m[warp] = mb;
-  }
-  __syncthreads();
-  if constexpr (kNorm) ss = warp_sum(lane < warps ? part_ss[lane] : 0.f);
-  mb = __reduce_max_sync(0xffffffffu, lane < warps ? part_m[lane] : 0u);
-
   float rstd = 1.f;
   if constexpr (kNorm) {
     rstd = 1.f / sqrtf(ss / (float)p.d + p.eps);
-    // the squares of values over 1e19 or under 1e-19 leave fp32's range: sum them in fp64
-    // (the same for all threads of the block)
-    if (!(ss > 1e-30f && ss < 3e38f)) {
-      double dd = 0.0;
+    if (wide && dd != 0.0) rstd = (float)(1.0 / sqrt((dd + (double)ss) / p.d + (double)p.eps));
+    if (p.y != nullptr) {
+      __nv_bfloat16* y = p.y + row * p.y_stride;
 #pragma unroll
-      for (int n = 0; n < NV; ++n)
+      for (int n = 0; n < NV; ++n) {
+        const int e = W * (8 / W * n * nthr + tid);
+        float2 v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dd += (double)r[n][i] * r[n][i];
-      dd = warp_sum(dd);
-      if (lane == 0) part_d[warp] = dd;
-      __syncthreads();
-      dd = warp_sum(lane < warps ? part_d[lane] : 0.0);
-      rstd = (float)(1.0 / sqrt(dd / p.d + (double)p.eps));
-    }
-  }
-
-  if (kNorm && p.y != nullptr) {
-    __nv_bfloat16* y = p.y + row * p.y_stride;
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = r[n][i] * rstd * g[n][i];
-      if constexpr (kVec) {
-        const int e = 8 * (n * nthr + tid);
-        if (e < p.d) store8(y + e, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = (8 * n + i) * nthr + tid;
-          if (e < p.d) store1(y + e, v[i]);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = make_float2(t[n][i].x * rstd, t[n][i].y * rstd);
+        store_pairs<W>(y + e, step, d - e, v);
       }
     }
+    if (p.codes == nullptr) return;
   }
-  if (p.codes == nullptr) return;
   const float m = __uint_as_float(mb);
   const bool finite = mb < 0x7F800000u;
-  if (tid == 0)
+  if (tid == 0 && d > 0)
     p.scales[row] = !finite ? __uint_as_float(0x7FC00000u) : m > 0.f ? m * rstd / 127.f : 0.f;
-  // rows of very small values are scaled up by a power of two (exact), so that 127 / m is finite
-  const float lift = m < 1e-30f ? 0x1p64f : 1.f;
-  const float ml = m * lift, inv = finite && m > 0.f ? 127.f / ml : 0.f;
+  // below 1e-30, where 127 / m may overflow, every code is taken the slow way
+  const bool tiny = m > 0.f && m < 1e-30f;
+  const float inv = finite && m >= 1e-30f ? 127.f / m : 0.f;
   int8_t* codes = p.codes + row * p.codes_stride;
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
-    uint32_t c[8];
+    const int e = W * (8 / W * n * nthr + tid);
+    uint2 c = make_uint2(0u, 0u);
+    float2(&v)[4] = t[kNorm ? n : 0];
+    if constexpr (!kNorm) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = kNorm ? r[n][i] * g[n][i] : r[n][i];
-      c[i] = inv > 0.f ? code_of(t * lift, ml, inv) : 0u;
+      for (int i = 0; i < 4; ++i) v[i] = rx[n].pair(i);
     }
-    if constexpr (kVec) {
-      const int e = 8 * (n * nthr + tid);
-      if (e < p.d) {
-        const uint32_t lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-        const uint32_t hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
-        *reinterpret_cast<uint2*>(codes + e) = make_uint2(lo, hi);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = (8 * n + i) * nthr + tid;
-        if (e < p.d) codes[e] = (int8_t)(c[i] & 0xFFu);
-      }
-    }
+    if (finite) c = tiny ? exact_codes(v[0], v[1], v[2], v[3], m) : codes8(v, m, inv);
+    store_codes<W>(codes + e, step, d - e, c);
   }
 }
 
-bool rows_aligned(const void* p, int64_t stride, int elem, int rows_bytes) {
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % rows_bytes == 0 && stride * elem % rows_bytes == 0);
+template <typename XT, typename RT, bool kNorm, int NV, int W, int G>
+cudaError_t launch_shape(const NormParams& p, cudaStream_t s) {
+  const auto kernel = norm_q8_kernel<XT, RT, kNorm, NV, W, G>;
+  if constexpr (G > 0) {
+    constexpr int kRows = kGroupThreads / G;
+    return launch_pdl(kernel, dim3((unsigned)((p.n_rows + kRows - 1) / kRows)), dim3(kGroupThreads), 0, s, p);
+  } else {
+    constexpr int per = 8 * NV;
+    return launch_pdl(kernel, dim3((unsigned)p.n_rows), dim3(((p.d + per - 1) / per + 31) / 32 * 32), 0, s, p);
+  }
+}
+
+// Rows with less than 16-byte alignment.
+template <typename XT, typename RT, bool kNorm, int W>
+cudaError_t launch_narrow(const NormParams& p, cudaStream_t s) {
+  if (p.d <= 256) return launch_shape<XT, RT, kNorm, 1, W, 32>(p, s);
+  if (p.d <= 512) return launch_shape<XT, RT, kNorm, 2, W, 32>(p, s);
+  if (p.d <= 1024) return launch_shape<XT, RT, kNorm, 4, W, 32>(p, s);
+  return launch_shape<XT, RT, kNorm, 2, W, 0>(p, s);
 }
 
 template <typename XT, typename RT, bool kNorm>
-cudaError_t launch_typed(const NormParams& p, int64_t n_rows, cudaStream_t s) {
+cudaError_t launch_typed(const NormParams& p, int num_sms, cudaStream_t s) {
   constexpr bool kRes = !std::is_same<RT, NoResidual>::value;
-  constexpr int res_size = kRes ? (std::is_same<RT, float>::value ? 4 : 2) : 1;
-  const bool vec = p.d % 8 == 0 && rows_aligned(p.x, p.x_stride, sizeof(XT), 16) &&
-                   rows_aligned(p.res, p.res_stride, res_size, 16) &&
-                   rows_aligned(p.res_out, p.res_out_stride, res_size, 16) &&
-                   rows_aligned(p.gamma, 0, 2, 16) && rows_aligned(p.y, p.y_stride, 2, 16) &&
-                   rows_aligned(p.codes, p.codes_stride, 1, 8);
-  const dim3 grid((unsigned)n_rows);
-  const bool one = vec && p.d <= 8192;   // a vector of 8 per thread, else two
-  const int per = one ? 8 : 16;
-  const int threads = std::max(32, ((p.d + per - 1) / per + 31) / 32 * 32);
-  if (one) return launch_pdl(norm_q8_kernel<XT, RT, kNorm, 1, true>, grid, dim3(threads), 0, s, p);
-  if (vec) return launch_pdl(norm_q8_kernel<XT, RT, kNorm, 2, true>, grid, dim3(threads), 0, s, p);
-  return launch_pdl(norm_q8_kernel<XT, RT, kNorm, 2, false>, grid, dim3(threads), 0, s, p);
+  constexpr int kResSize = kRes ? (std::is_same<RT, float>::value ? 4 : 2) : 1;
+  // the largest W for which d is a multiple and each row starts on W values or 16 bytes
+  int w = 8;
+  const auto fit = [&w](const void* q, int64_t stride, int elem) {
+    while (q != nullptr && w > 1) {
+      const int bytes = std::min(16, w * elem);
+      if (reinterpret_cast<uintptr_t>(q) % bytes == 0 && stride * elem % bytes == 0) break;
+      w /= 2;
+    }
+  };
+  while (p.d % w != 0) w /= 2;
+  fit(p.x, p.x_stride, sizeof(XT));
+  fit(p.res, p.res_stride, kResSize);
+  fit(p.res_out, p.res_out_stride, kResSize);
+  fit(p.gamma, 0, 2);
+  fit(p.y, p.y_stride, 2);
+  fit(p.codes, p.codes_stride, 1);
+  if (w == 4) return launch_narrow<XT, RT, kNorm, 4>(p, s);
+  if (w == 2) return launch_narrow<XT, RT, kNorm, 2>(p, s);
+  if (w == 1) return launch_narrow<XT, RT, kNorm, 1>(p, s);
+  if (p.d <= 64) return launch_shape<XT, RT, kNorm, 1, 8, 8>(p, s);
+  if (p.d <= 128) return launch_shape<XT, RT, kNorm, 1, 8, 16>(p, s);
+  if (p.d <= 256) return launch_shape<XT, RT, kNorm, 1, 8, 32>(p, s);
+  if (p.d <= 512) return launch_shape<XT, RT, kNorm, 2, 8, 32>(p, s);
+  if (p.d <= 768) return launch_shape<XT, RT, kNorm, 3, 8, 32>(p, s);
+  if (p.d <= 1024) return launch_shape<XT, RT, kNorm, 4, 8, 32>(p, s);
+  // Block per row. A row alone on its SM is bound by latency, and more threads with a vector each
+  // shorten it (1 x 5120: 1.95 against 2.3 us). Many rows want two vectors in flight per thread
+  // (2441 x 8192 bf16: 16.1 against 25.7 us), and past 8192 values four with half the threads, so
+  // that a row loads while another is stored (1220 x 16384 bf16: 15.5 against 18.4 us), but not
+  // where x and residual in fp32 would spill (46.5 against 54.2 us) or one wave takes all rows.
+  if (p.n_rows <= num_sms && p.d <= 8192) return launch_shape<XT, RT, kNorm, 1, 8, 0>(p, s);
+  constexpr bool kWide = kRes && sizeof(XT) == 4 && kResSize == 4;
+  if constexpr (!kWide)
+    if (p.d > 8192 && p.n_rows > 4 * num_sms) return launch_shape<XT, RT, kNorm, 4, 8, 0>(p, s);
+  return launch_shape<XT, RT, kNorm, 2, 8, 0>(p, s);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_q8(const NormArgs& a, cudaStream_t s) {
+cudaError_t launch_norm_q8(const mla_decode_s& h, const NormArgs& a, cudaStream_t s) {
   NormParams p{};
+  p.n_rows = a.n_rows;
   p.x = a.x;
   p.res = a.residual;
   p.res_out = a.residual_out;
@@ -252,17 +450,15 @@ cudaError_t launch_norm_q8(const NormArgs& a, cudaStream_t s) {
   p.codes_stride = a.codes_stride;
   p.d = a.d;
   p.eps = a.eps;
+  using BF = __nv_bfloat16;
+  const int sms = h.num_sms;
   if (a.gamma == nullptr)
-    return a.x_f32 ? launch_typed<float, NoResidual, false>(p, a.n_rows, s)
-                   : launch_typed<__nv_bfloat16, NoResidual, false>(p, a.n_rows, s);
+    return a.x_f32 ? launch_typed<float, NoResidual, false>(p, sms, s) : launch_typed<BF, NoResidual, false>(p, sms, s);
   if (a.residual == nullptr)
-    return a.x_f32 ? launch_typed<float, NoResidual, true>(p, a.n_rows, s)
-                   : launch_typed<__nv_bfloat16, NoResidual, true>(p, a.n_rows, s);
+    return a.x_f32 ? launch_typed<float, NoResidual, true>(p, sms, s) : launch_typed<BF, NoResidual, true>(p, sms, s);
   if (a.residual_f32)
-    return a.x_f32 ? launch_typed<float, float, true>(p, a.n_rows, s)
-                   : launch_typed<__nv_bfloat16, float, true>(p, a.n_rows, s);
-  return a.x_f32 ? launch_typed<float, __nv_bfloat16, true>(p, a.n_rows, s)
-                 : launch_typed<__nv_bfloat16, __nv_bfloat16, true>(p, a.n_rows, s);
+    return a.x_f32 ? launch_typed<float, float, true>(p, sms, s) : launch_typed<BF, float, true>(p, sms, s);
+  return a.x_f32 ? launch_typed<float, BF, true>(p, sms, s) : launch_typed<BF, BF, true>(p, sms, s);
 }
 
 }  // namespace mla

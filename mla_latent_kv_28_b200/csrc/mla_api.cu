@@ -126,6 +126,7 @@ int mla_decode_create(const mla_config_t* cfg, int device, mla_handle_t* out) {
   const size_t o_useq = off;      off = round_up(off + 4 * max_units, 256);
   const size_t o_plse = off;      off = round_up(off + 4 * (size_t)max_slots * h->group_rows, 256);
   const size_t o_po = off;        off = round_up(off + 4 * (size_t)max_slots * h->group_rows * kDLatent, 256);
+  const size_t o_turns = off;     off = round_up(off + 8 * (kDRope / 2), 256);
   const size_t o_ap = off;        off = round_up(off + 4 * (size_t)mla::kAppendSlices * B * h->q_len * mla::kRow, 256);
 
   void* base = nullptr;
@@ -153,6 +154,17 @@ int mla_decode_create(const mla_config_t* cfg, int device, mla_handle_t* out) {
   h->ws.part_lse = reinterpret_cast<float*>(p + o_plse);
   h->ws.part_o = reinterpret_cast<float*>(p + o_po);
   h->ws.append_part = reinterpret_cast<float*>(p + o_ap);
+  h->ws.turns = reinterpret_cast<uint64_t*>(p + o_turns);
+  uint64_t turns[kDRope / 2];   // whole turns per token change nothing: positions are integers
+  for (int m = 0; m < kDRope / 2; ++m) {
+    const double t = h->theta[m] / 6.283185307179586476925;
+    turns[m] = (uint64_t)std::ldexp(t - std::floor(t), 64);
+  }
+  if (cudaMemcpy(h->ws.turns, turns, sizeof(turns), cudaMemcpyHostToDevice) != cudaSuccess) {
+    cudaFree(base);
+    delete h;
+    return MLA_ERR_CUDA;
+  }
   h->ws.max_units = max_units;
   h->ws.max_slots = max_slots;
   *out = h;

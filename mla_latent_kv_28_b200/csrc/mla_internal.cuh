@@ -56,6 +56,7 @@ struct Workspace {
   float* part_o = nullptr;   // [max_slots, 128 quads, n_h, 4] partial latent outputs (normalised)
   float* part_lse = nullptr; // [max_slots, n_h]     their log-sum-exp
   float* append_part = nullptr;  // [kAppendSlices, max_batch, 576] the cache write's partial sums
+  uint64_t* turns = nullptr;     // [32] RoPE pair frequencies over 2 pi, the part of a turn in 2^-64
   int max_units = 0;
   int max_slots = 0;
 };

@@ -50,111 +50,6 @@ struct NormParams {
 
 struct NoResidual {};
 
-// max(a, |b|, |c|), and NaN if one of them is
-__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float max_abs(float a, float b, float c) {
-  float d;
-  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// Eight values as loaded, in pairs: W neighbouring ones at p, W more at p + step, and so on while
-// they lie before `left` values from p.
-template <typename T, int W>
-struct Raw8;
-template <int W>
-struct Raw8<__nv_bfloat16, W> {
-  uint32_t w[4];
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, int step, int left) {
-#pragma unroll
-    for (int c = 0; c < 8 / W; ++c) {
-      const __nv_bfloat16* q = p + (int64_t)c * step;
-      const bool in = c * step < left;
-      if constexpr (W == 8) {
-        const uint4 u = in ? *reinterpret_cast<const uint4*>(q) : make_uint4(0, 0, 0, 0);
-        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-      } else if constexpr (W == 4) {
-        const uint2 u = in ? *reinterpret_cast<const uint2*>(q) : make_uint2(0, 0);
-        w[2 * c] = u.x; w[2 * c + 1] = u.y;
-      } else if constexpr (W == 2) {
-        w[c] = in ? *reinterpret_cast<const uint32_t*>(q) : 0u;
-      } else {
-        const uint32_t u = in ? *reinterpret_cast<const uint16_t*>(q) : 0u;
-        w[c >> 1] = c & 1 ? w[c >> 1] | u << 16 : u;
-      }
-    }
-  }
-  __device__ __forceinline__ float2 pair(int i) const {
-    return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-  }
-};
-template <int W>
-struct Raw8<float, W> {
-  float2 v[4];
-  __device__ __forceinline__ void load(const float* p, int step, int left) {
-#pragma unroll
-    for (int c = 0; c < 8 / W; ++c) {
-      const float* q = p + (int64_t)c * step;
-      const bool in = c * step < left;
-      if constexpr (W >= 4) {
-#pragma unroll
-        for (int h = 0; h < W / 4; ++h) {
-          const float4 a = in ? reinterpret_cast<const float4*>(q)[h] : make_float4(0.f, 0.f, 0.f, 0.f);
-          v[c * W / 2 + 2 * h] = make_float2(a.x, a.y);
-          v[c * W / 2 + 2 * h + 1] = make_float2(a.z, a.w);
-        }
-      } else if constexpr (W == 2) {
-        v[c] = in ? *reinterpret_cast<const float2*>(q) : make_float2(0.f, 0.f);
-      } else {
-        const float a = in ? *q : 0.f;
-        if (c & 1) v[c >> 1].y = a;
-        else v[c >> 1].x = a;
-      }
-    }
-  }
-  __device__ __forceinline__ float2 pair(int i) const { return v[i]; }
-};
-
-template <int W>
-__device__ __forceinline__ void store_pairs(float* p, int step, int left, const float2 (&v)[4]) {
-#pragma unroll
-  for (int c = 0; c < 8 / W; ++c) {
-    if (c * step >= left) continue;
-    float* q = p + (int64_t)c * step;
-    if constexpr (W >= 4) {
-#pragma unroll
-      for (int h = 0; h < W / 4; ++h) {
-        const float2 a = v[c * W / 2 + 2 * h], b = v[c * W / 2 + 2 * h + 1];
-        reinterpret_cast<float4*>(q)[h] = make_float4(a.x, a.y, b.x, b.y);
-      }
-    } else if constexpr (W == 2) {
-      *reinterpret_cast<float2*>(q) = v[c];
-    } else {
-      *q = c & 1 ? v[c >> 1].y : v[c >> 1].x;
-    }
-  }
-}
-template <int W>
-__device__ __forceinline__ void store_pairs(__nv_bfloat16* p, int step, int left, const float2 (&v)[4]) {
-#pragma unroll
-  for (int c = 0; c < 8 / W; ++c) {
-    if (c * step >= left) continue;
-    __nv_bfloat16* q = p + (int64_t)c * step;
-    if constexpr (W == 8)
-      *reinterpret_cast<uint4*>(q) = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
-                                                pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
-    else if constexpr (W == 4)
-      *reinterpret_cast<uint2*>(q) = make_uint2(pack_bf16(v[2 * c].x, v[2 * c].y), pack_bf16(v[2 * c + 1].x, v[2 * c + 1].y));
-    else if constexpr (W == 2)
-      *reinterpret_cast<uint32_t*>(q) = pack_bf16(v[c].x, v[c].y);
-    else
-      *q = __float2bfloat16_rn(c & 1 ? v[c >> 1].y : v[c >> 1].x);
-  }
-}
 template <int W>
 __device__ __forceinline__ void store_codes(int8_t* p, int step, int left, uint2 v) {
 #pragma unroll
@@ -283,7 +178,7 @@ norm_q8_kernel(const NormParams p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 g = rg[n].pair(i);
-        t[n][i] = make_float2(t[n][i].x * g.x, t[n][i].y * g.y);
+        t[n][i] = sm100::fmul2(t[n][i], g);
       }
       st.largest(t[n]);
     }
@@ -341,7 +236,7 @@ norm_q8_kernel(const NormParams p) {
         const int e = W * (8 / W * n * nthr + tid);
         float2 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = make_float2(t[n][i].x * rstd, t[n][i].y * rstd);
+        for (int i = 0; i < 4; ++i) v[i] = sm100::fmul2(t[n][i], make_float2(rstd, rstd));
         store_pairs<W>(y + e, step, d - e, v);
       }
     }

@@ -4,19 +4,26 @@
 // so a result does not depend on how the sum is split; it is rounded when it becomes fp32, at each
 // of the two scales, and to the output's type.
 //
-// Few tokens (linear_few): bound by reading the weights. A cluster takes 128 output channels (the
-// M = 128 operand) times up to 128 tokens (N); its CTAs share the sum's length, each streaming its
-// part of the weights through a ring of TMA boxes into tcgen05 MMAs (kind::i8, int32 in tensor
-// memory), and meet in distributed shared memory, where each adds and scales a part of the tile.
+// Up to 128 tokens (linear_few): bound by reading the weights. A cluster takes 128 output channels (the
+// M = 128 operand) times all tokens (N); its CTAs share the sum's length, each streaming its part of the
+// weights through a ring of TMA boxes into tcgen05 MMAs (kind::i8, int32 in tensor memory). Each CTA then
+// sends its partial sums to the CTAs that finish them (asynchronous stores into their shared memory,
+// counted by a barrier there: no second meeting), which add, scale and store. 33 x 16384 -> 5120 18.6 us
+// (4500 GB/s), 64 x 1536 -> 16384 9.0 us, 1 x 5120 -> 2112 5.4 to 6.0 us.
 //
-// Many tokens (linear_many): bound by the tensor core. A pair of CTAs (cta_group::2) takes 256
-// tokens x up to 256 channels: each CTA holds 128 of the tokens and half of the channels, so a
-// pair reads 64 KB per 128 steps of k for 256 x 256 results. Persistent, with the accumulator
-// double-buffered in tensor memory: eight warps scale and store a tile while the next is summed.
+// More tokens (linear_many): bound by the tensor core, and by the power that it takes. A pair of CTAs
+// (cta_group::2) takes 256 tokens x up to 256 channels: each CTA holds 128 of the tokens and half of the
+// channels, so a pair reads 64 KB per 128 steps of k for 256 x 256 results. Persistent, with the
+// accumulator double-buffered in tensor memory: eight warps scale and store a tile while the next is
+// summed. 2048 x 16384 -> 5120 116 us (2960 TOP/s; 136 us at the clocks of a long run), 8192 x 1536 ->
+// 8192 87 us (2370 TOP/s, its 128 MB of results beside it), 333 x 1000 -> 777 7 us.
+//
+// In both the loops that issue copies and MMAs are run by whole warps with one elected lane, so that
+// descriptors and barriers stay in uniform registers: with a lone thread the 730 cycles of its own
+// instructions per k block were what bound them (512 of MMA).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "mla_internal.cuh"
 #include "rows.cuh"
@@ -29,42 +36,83 @@ using namespace sm100;
 
 constexpr int kBoxK = 128;                      // codes (bytes) of k per box: one swizzle row
 constexpr uint32_t kWBox = 128 * kBoxK;         // 128 rows of a box
-constexpr int kMaxSplits = 8;                   // portable cluster size
+constexpr int kFewRows = 128;                   // tokens of linear_few: the MMA's N, in one piece
+constexpr int kMaxFewStages = 12;
 constexpr long long kWaitLimit = 2000000000LL;  // cycles: about a second
+
+// One lane of the warp, the same for all calls, so that what the loops below keep is uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// A ring position: the stage and how often the ring has been passed, mod 2.
+struct RingPos {
+  uint32_t stage = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t stages) {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// wait_bounded by a whole warp, with one answer for it, whose first probe takes no clock: a ring's stages
+// follow each other within a few hundred cycles, and the issuing warps' own instructions count.
+__device__ __forceinline__ bool wait_ring(uint32_t bar, uint32_t parity, const WaitGuard& g) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, g));
+}
 
 struct FewParams {
   int rows, n, n_tile, splits, kblocks, stages;
-  uint32_t ring;         // bytes of the ring, at least those of the partial tile
+  uint32_t ring;         // bytes of the ring
   uint32_t idesc;
   const float* a_scale;
   const float* w_scale;
   void* out;
   int64_t out_stride;
-  bool vec;              // 4 neighbouring outputs can be stored at once
   uint32_t* err;
 };
 
-__device__ __forceinline__ void store4(float* p, const float (&v)[4], int n, bool vec) {
-  if (vec && n >= 4) {
+// n of 4 neighbouring outputs (their rows are aligned for 4).
+__device__ __forceinline__ void store4(float* p, const float (&v)[4], int n) {
+  if (n >= 4) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
     return;
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 3; ++j)
     if (j < n) p[j] = v[j];
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4], int n, bool vec) {
-  if (vec && n >= 4) {
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4], int n) {
+  if (n >= 4) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     return;
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 3; ++j)
     if (j < n) p[j] = __float2bfloat16_rn(v[j]);
 }
 
-// smem: ring of stages [128 x 128 weight box | n_tile x 128 token box], then the barriers. The
-// ring is reused for the CTA's partial sums [token][128 channels] once its MMAs are done.
+// The scales of columns col (and, if all, the three behind it) that lie before end.
+__device__ __forceinline__ void load_scales(float (&w)[4], const float* scales, int col, int end, bool all) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = (j == 0 || all) && col + j < end ? scales[col + j] : 0.f;
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// smem: ring of stages [128 x 128 weight box | n_tile x 128 token box], the partial sums that this CTA
+// receives, the barriers. Of the tile's 128 channels CTA r of the cluster finishes those from
+// ceil(128 r / splits) on: it gets from each CTA [its channels][4 tokens] pieces of 16 bytes, a
+// channel's pieces an odd number of 16-byte units from the next one's (no bank conflicts).
 template <typename OT>
 __global__ void __launch_bounds__(256)
 linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
@@ -72,26 +120,31 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t stage_bytes = kWBox + (uint32_t)p.n_tile * kBoxK;
-  const uint32_t bars = sbase + p.ring;   // full[stages], empty[stages], done
-  const uint32_t done = bars + 16 * p.stages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (done + 8 - sbase));
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (done + 12 - sbase));
+  const uint32_t stages = p.stages, stage_bytes = kWBox + (uint32_t)p.n_tile * kBoxK;
+  const uint32_t full = sbase, empty = full + 8 * kMaxFewStages, done = empty + 8 * kMaxFewStages, received = done + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 16 * kMaxFewStages + 16);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 16 * kMaxFewStages + 20);
+  const uint32_t ring = sbase + 1024, parts = ring + p.ring;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = p.splits > 1 ? (int)cluster_ctarank() : 0;
-  const int f0 = (blockIdx.x / p.splits) * 128, t0 = blockIdx.y * p.n_tile;
-  const int kb0 = (int)((int64_t)p.kblocks * rank / p.splits);
-  const int kb1 = (int)((int64_t)p.kblocks * (rank + 1) / p.splits);
-  const uint32_t tmem_cols = p.n_tile < 32 ? 32u : (uint32_t)p.n_tile;   // a power of two
+  const int splits = p.splits, rank = splits > 1 ? (int)cluster_ctarank() : 0;
+  const int f0 = (blockIdx.x / splits) * 128;
+  const int kb0 = (int)((int64_t)p.kblocks * rank / splits), kb1 = (int)((int64_t)p.kblocks * (rank + 1) / splits);
+  const uint32_t tmem_cols = p.n_tile <= 32 ? 32u : p.n_tile <= 64 ? 64u : 128u;
+  const int rows = p.rows, quads = (rows + 3) / 4;
+  const int c_begin = (128 * rank + splits - 1) / splits, c_count = (128 * (rank + 1) + splits - 1) / splits - c_begin;
+  const uint32_t pitch = (uint32_t)(quads | 1) * 16;          // bytes between a part's channels
+  const uint32_t part = (uint32_t)((128 + splits - 1) / splits) * pitch;   // ... between the parts
   const WaitGuard guard{abort_flag, p.err, kErrTimeout, kWaitLimit};
 
   if (tid == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(bars + 8 * s, 1);
-      mbar_init(bars + 8 * (p.stages + s), 1);
+    for (uint32_t s = 0; s < stages; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
     }
     mbar_init(done, 1);
+    mbar_init(received, 1);
     fence_mbarrier_init_cluster();
+    if (splits > 1) mbar_arrive_expect_tx(received, (uint32_t)(splits * c_count * quads * 16));
     *abort_flag = 0;
     prefetch_tmap(&tmap_w);
     prefetch_tmap(&tmap_a);
@@ -104,103 +157,123 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
   }
   tc_fence_before();
   __syncthreads();
+  if (splits > 1) cluster_arrive();   // this CTA may be written to
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();
   allow_dependent_launch();
 
-  if (tid == 0) {
+  if (warp == 0) {
+    RingPos at;
     int issued = 0;
     for (int kb = kb0; kb < kb1; ++kb, ++issued) {
-      const int s = issued % p.stages;
-      if (!wait_bounded(bars + 8 * (p.stages + s), ((issued / p.stages) & 1) ^ 1, guard)) break;
-      const uint32_t full = bars + 8 * s, dst = sbase + s * stage_bytes;
-      mbar_arrive_expect_tx(full, stage_bytes);
-      tma_load_2d(dst, &tmap_w, kb * kBoxK, f0, full);
-      tma_load_2d(dst + kWBox, &tmap_a, kb * kBoxK, t0, full);
+      if (!wait_ring(empty + 8 * at.stage, at.phase ^ 1, guard)) break;
+      if (elect_one()) {
+        const uint32_t bar = full + 8 * at.stage, dst = ring + at.stage * stage_bytes;
+        mbar_arrive_expect_tx(bar, stage_bytes);
+        tma_load_2d(dst, &tmap_w, kb * kBoxK, f0, bar);
+        tma_load_2d(dst + kWBox, &tmap_a, kb * kBoxK, 0, bar);
+      }
+      at.next(stages);
     }
     if (*abort_flag) {   // never leave with copies in flight
-      for (int u = std::max(0, issued - p.stages); u < issued; ++u) {
+      for (int u = max(0, issued - p.stages); u < issued; ++u) {
         const long long t = clock64();
-        while (!mbar_test(bars + 8 * (u % p.stages), (u / p.stages) & 1) && clock64() - t < kWaitLimit) {}
+        while (!mbar_test(full + 8 * (u % p.stages), (u / p.stages) & 1) && clock64() - t < kWaitLimit) {}
       }
     }
-  } else if (warp == 1 && lane == 0) {
-    for (int u = 0; u < kb1 - kb0; ++u) {
-      const int s = u % p.stages;
-      if (!wait_bounded(bars + 8 * s, (u / p.stages) & 1, guard)) break;
+  } else if (warp == 1) {
+    RingPos at;
+    const uint64_t w_desc = smem_desc(ring, 16, 1024, 2), a_desc = smem_desc(ring + kWBox, 16, 1024, 2);
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!wait_ring(full + 8 * at.stage, at.phase, guard)) break;
       tc_fence_after();
-      const uint32_t w = sbase + s * stage_bytes, a = w + kWBox;
+      const uint64_t off = (at.stage * stage_bytes) >> 4;
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mma_i8_ss(tmem, smem_desc(w + 32 * k, 16, 1024, 2), smem_desc(a + 32 * k, 16, 1024, 2), p.idesc,
-                  (u | k) != 0 ? 1u : 0u);
-      mma_commit(bars + 8 * (p.stages + s));
+        for (int k = 0; k < 4; ++k)   // 32 codes each
+          mma_i8_ss(tmem, w_desc + off + 2 * k, a_desc + off + 2 * k, p.idesc, kb != kb0 || k != 0 ? 1u : 0u);
+        mma_commit(empty + 8 * at.stage);
+      }
+      at.next(stages);
     }
-    mma_commit(done);
+    if (elect_one()) mma_commit(done);
   }
   __syncwarp();
-  wait_bounded(done, 0, guard);
-  tc_fence_after();
-  // wait_bounded returns per thread; the warp-wide loads below need the warp together
+  bool ok = wait_bounded(done, 0, guard);
   __syncwarp();
-  // (all boxes of this CTA have been read by its MMAs: the ring is free)
-  {
-    int32_t* part = reinterpret_cast<int32_t*>(smem);
-    const int f = 32 * (warp & 3) + lane;
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const int cols = p.n_tile < 16 ? 16 : p.n_tile;
-    for (int c0 = 16 * (warp >> 2); c0 < cols; c0 += 32) {
+  tc_fence_after();
+
+  const int f = 32 * (warp & 3) + lane;   // this lane's channel of the tile
+  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+  if (splits == 1) {
+    const float w = f0 + f < p.n ? p.w_scale[f0 + f] : 0.f;
+    for (int c0 = 16 * (warp >> 2); c0 < rows; c0 += 32) {
+      uint32_t r[16];
+      tmem_ld16_sync(lanes | (tmem + c0), r);
+      OT* out = static_cast<OT*>(p.out) + (int64_t)c0 * p.out_stride + f0 + f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (c0 + j < rows && f0 + f < p.n)
+          store1(out + j * p.out_stride, (float)(int32_t)r[j] * w * p.a_scale[c0 + j]);
+    }
+  } else {
+    const int owner = f * splits >> 7, c = f - (128 * owner + splits - 1) / splits;
+    cluster_wait();   // the others have set their barriers up
+    const uint32_t to = map_to_rank(parts + rank * part + c * pitch, owner), bar = map_to_rank(received, owner);
+    for (int c0 = 16 * (warp >> 2); c0 < rows; c0 += 32) {
       uint32_t r[16];
       tmem_ld16_sync(lanes | (tmem + c0), r);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) part[(c0 + j) * 128 + f] = (int32_t)r[j];
+      for (int j = 0; j < 4; ++j)
+        if (c0 + 4 * j < rows) st_async_v4(to + (c0 / 4 + j) * 16, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3], bar);
+    }
+    ok = wait_bounded(received, 0, guard, true) && ok;
+    const int count = min(c_count, p.n - f0 - c_begin);   // may be negative
+    if (ok && count > 0) {
+      for (int it = tid; it < count * quads; it += 256) {
+        const int q = it / count, ch = it - q * count, col = f0 + c_begin + ch;
+        int32_t acc[4] = {0, 0, 0, 0};
+        const uint8_t* from = smem + (parts - sbase) + ch * pitch + q * 16;
+        for (int src = 0; src < splits; ++src) {
+          const int4 v = *reinterpret_cast<const int4*>(from + src * part);
+          acc[0] += v.x; acc[1] += v.y; acc[2] += v.z; acc[3] += v.w;
+        }
+        const float w = p.w_scale[col];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = 4 * q + j;
+          if (t < rows)
+            store1(static_cast<OT*>(p.out) + (int64_t)t * p.out_stride + col, (float)acc[j] * w * p.a_scale[t]);
+        }
+      }
     }
   }
   tc_fence_before();
-  if (p.splits > 1) cluster_sync();
-  else __syncthreads();
-
-  const int rows = min(p.n_tile, p.rows - t0);
-  const int items = rows * 32;   // 4 channels of one token each
-  for (int it = rank * 256 + tid; it < items; it += 256 * p.splits) {
-    const int t = it >> 5, q = it & 31, f = f0 + 4 * q;
-    if (f >= p.n) continue;
-    int32_t acc[4] = {0, 0, 0, 0};
-    const uint32_t at = sbase + (uint32_t)it * 16;
-    for (int s = 0; s < p.splits; ++s) {
-      int4 v;
-      ld_cluster_v4(p.splits > 1 ? map_to_rank(at, s) : at, v);
-      acc[0] += v.x; acc[1] += v.y; acc[2] += v.z; acc[3] += v.w;
-    }
-    const float as = p.a_scale[t0 + t];
-    float o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = f + j < p.n ? (float)acc[j] * p.w_scale[f + j] * as : 0.f;
-    store4(static_cast<OT*>(p.out) + (int64_t)(t0 + t) * p.out_stride + f, o, p.n - f, p.vec);
-  }
-  if (p.splits > 1) cluster_sync();   // no CTA leaves while another reads its shared memory
-  else __syncthreads();
+  const bool failed = __syncthreads_or(!ok);
+  tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, tmem_cols);
+  // having received from every CTA, none writes here any more; after a wait that ran out one might
+  if (failed && splits > 1) cluster_sync();
 }
 
 // ------------------------------------------------------------------ many tokens
 
-constexpr int kManyStages = 6;
-constexpr uint32_t kManyStage = 2 * kWBox;                  // 128 tokens + up to 128 channels
+constexpr int kMaxManyStages = 10;
+constexpr uint32_t kManyRing = 12 * kWBox;                  // 128 tokens + up to 128 channels a stage
 constexpr int kEpiWarps = 8;
 constexpr uint32_t kEpiBox = 32 * 128;                      // 32 rows x 128 bytes per warp
 constexpr int kManyThreads = 32 * (4 + kEpiWarps);
-constexpr uint32_t kManySmem = kManyStages * kManyStage + kEpiWarps * kEpiBox + 256 + 1024;
+constexpr uint32_t kManySmem = kManyRing + kEpiWarps * kEpiBox + 256 + 1024;
 
 struct ManyParams {
-  int rows, n, n_tile, kblocks, tiles_m, tiles_n, group;
+  int rows, n, n_tile, kblocks, tiles_m, tiles_n, group, stages;
   uint32_t idesc;
   const float* a_scale;
   const float* w_scale;
   void* out;
   int64_t out_stride;
-  bool vec;              // rows of the output are 16-byte aligned
+  bool vec;              // 4 neighbouring outputs can be stored at once
   uint32_t* err;
 };
 
@@ -220,9 +293,10 @@ linear_many(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t epi = kManyStages * kManyStage;
+  const uint32_t epi = kManyRing, stage_bytes = kWBox + (uint32_t)p.n_tile / 2 * kBoxK;
+  const uint32_t stages = p.stages;
   const uint32_t bars = sbase + epi + kEpiWarps * kEpiBox;
-  const uint32_t full = bars, empty = bars + 8 * kManyStages, acc_full = empty + 8 * kManyStages,
+  const uint32_t full = bars, empty = bars + 8 * kMaxManyStages, acc_full = empty + 8 * kMaxManyStages,
                  acc_empty = acc_full + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (acc_empty + 16 - sbase));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (acc_empty + 20 - sbase));
@@ -233,7 +307,7 @@ linear_many(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
   const WaitGuard guard{abort_flag, p.err, kErrTimeout, kWaitLimit};
 
   if (tid == 0) {
-    for (int s = 0; s < kManyStages; ++s) {
+    for (uint32_t s = 0; s < stages; ++s) {
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, 1);
     }
@@ -258,133 +332,139 @@ linear_many(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
   allow_dependent_launch();
 
   const uint32_t half_n = (uint32_t)p.n_tile / 2;
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // producer: this CTA's tokens and its half of the channels; both CTAs' copies count toward
     // the first CTA's barrier, where the MMAs are issued
-    const uint32_t bytes = 2 * (kWBox + half_n * kBoxK);
+    const uint32_t bytes = 2 * (kWBox + half_n * kBoxK), lead_full = map_to_rank(full, 0);
+    RingPos at;
     int u = 0;
-    for (int t = cluster; t < tiles && !*abort_flag; t += clusters) {
+    bool ok = true;
+    for (int t = cluster; t < tiles && ok; t += clusters) {
       int tm, tn;
       tile_at(p, t, tm, tn);
       const int y_a = tm * 256 + (int)rank * 128, y_w = tn * p.n_tile + (int)(rank * half_n);
       for (int kb = 0; kb < p.kblocks; ++kb, ++u) {
-        const int s = u % kManyStages;
-        if (!wait_bounded(empty + 8 * s, ((u / kManyStages) & 1) ^ 1, guard)) break;
-        if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
-        const uint32_t bar = map_to_rank(full + 8 * s, 0), dst = sbase + s * kManyStage;
-        tma_load_2d_pair(dst, &tmap_a, kb * kBoxK, y_a, bar);
-        tma_load_2d_pair(dst + kWBox, &tmap_w, kb * kBoxK, y_w, bar);
+        if (!(ok = wait_ring(empty + 8 * at.stage, at.phase ^ 1, guard))) break;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * at.stage, bytes);
+          const uint32_t bar = lead_full + 8 * at.stage, dst = sbase + at.stage * stage_bytes;
+          tma_load_2d_pair(dst, &tmap_a, kb * kBoxK, y_a, bar);
+          tma_load_2d_pair(dst + kWBox, &tmap_w, kb * kBoxK, y_w, bar);
+        }
+        at.next(stages);
       }
     }
     // the last boxes have been read, so no copy and no signal is still on its way to this CTA
-    for (int v = max(0, u - kManyStages); v < u; ++v)
-      if (!wait_bounded(empty + 8 * (v % kManyStages), (v / kManyStages) & 1, guard)) break;
+    const int ring = (int)stages;
+    for (int v = max(0, u - ring); v < u; ++v)
+      if (!wait_bounded(empty + 8 * (v % ring), (v / ring) & 1, guard)) break;
     if (*abort_flag && rank == 0) {   // bounded: let both CTAs' copies land
-      for (int v = max(0, u - kManyStages); v < u; ++v) {
+      for (int v = max(0, u - ring); v < u; ++v) {
         const long long t0 = clock64();
-        while (!mbar_test(full + 8 * (v % kManyStages), (v / kManyStages) & 1) && clock64() - t0 < kWaitLimit) {}
+        while (!mbar_test(full + 8 * (v % ring), (v / ring) & 1) && clock64() - t0 < kWaitLimit) {}
       }
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
-    int u = 0, it = 0;
-    for (int t = cluster; t < tiles && !*abort_flag; t += clusters, ++it) {
+  } else if (warp == 1 && rank == 0) {
+    RingPos at;
+    int it = 0;
+    bool ok = true;
+    const uint64_t a_desc = smem_desc(sbase, 16, 1024, 2), w_desc = smem_desc(sbase + kWBox, 16, 1024, 2);
+    for (int t = cluster; t < tiles && ok; t += clusters, ++it) {
       const int as = it & 1;
-      if (!wait_bounded(acc_empty + 8 * as, ((it >> 1) & 1) ^ 1, guard, true)) break;
+      if (!__all_sync(0xffffffffu, wait_bounded(acc_empty + 8 * as, ((it >> 1) & 1) ^ 1, guard, true))) break;
       tc_fence_after();
-      bool ok = true;
-      for (int kb = 0; kb < p.kblocks; ++kb, ++u) {
-        const int s = u % kManyStages;
-        if (!(ok = wait_bounded(full + 8 * s, (u / kManyStages) & 1, guard))) break;
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        if (!(ok = wait_ring(full + 8 * at.stage, at.phase, guard))) break;
         tc_fence_after();
-        const uint32_t a = sbase + s * kManyStage, w = a + kWBox;
+        const uint64_t off = (at.stage * stage_bytes) >> 4;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_i8_ss_pair(tmem + 256 * as, smem_desc(a + 32 * k, 16, 1024, 2), smem_desc(w + 32 * k, 16, 1024, 2),
-                         p.idesc, (kb | k) != 0 ? 1u : 0u);
-        mma_commit_pair(empty + 8 * s);
+          for (int k = 0; k < 4; ++k)   // 32 codes each
+            mma_i8_ss_pair(tmem + 256 * as, a_desc + off + 2 * k, w_desc + off + 2 * k, p.idesc,
+                           (kb | k) != 0 ? 1u : 0u);
+          mma_commit_pair(empty + 8 * at.stage);
+        }
+        at.next(stages);
       }
-      if (!ok) break;
-      mma_commit_pair(acc_full + 8 * as);
+      if (ok && elect_one()) mma_commit_pair(acc_full + 8 * as);
     }
   } else if (warp >= 4) {
-    // epilogue: warp w reads tensor memory lanes 32 (w % 4) .. + 32 (one token each) and half of
-    // the tile's columns, a box of 32 tokens x 128 bytes at a time
-    constexpr int kCols = 128 / (int)sizeof(OT);   // columns per box
-    const int quarter = warp & 3, part = (warp - 4) >> 2;
+    // epilogue: warp w reads tensor memory lanes 32 (w % 4) .. + 32 (one token each) and half of the
+    // tile's columns, 32 at a time, and turns each 32 x 32 block round in shared memory (16-byte units,
+    // swizzled so that both directions are free of conflicts), so that a lane keeps its columns' scales
+    // and rows are written in whole sectors
+    const int quarter = warp & 3, per = p.n_tile / 2, first = ((warp - 4) >> 2) * per;
     const uint32_t box = sbase + epi + (uint32_t)(warp - 4) * kEpiBox;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    const int per = p.n_tile / 2;
     int it = 0;
     for (int t = cluster; t < tiles; t += clusters, ++it) {
       int tm, tn;
       tile_at(p, t, tm, tn);
-      const int as = it & 1;
+      const int as = it & 1, row0 = tm * 256 + (int)rank * 128 + 32 * quarter;
+      // the scales arrive while the tile is summed: the token's, and those of this lane's column (or 4)
+      // of the first 32; the next 32 columns' follow while these are worked on
+      const float a_scale = row0 + lane < p.rows ? p.a_scale[row0 + lane] : 0.f;
+      const int begin = tn * p.n_tile + first, end = min(p.n, begin + per);
+      int col = begin + (p.vec ? 4 * (lane & 7) : lane);   // this lane's (first) column
+      float w[4];
+      load_scales(w, p.w_scale, col, end, p.vec);
       const bool ok = wait_bounded(acc_full + 8 * as, (it >> 1) & 1, guard);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const int row0 = tm * 256 + (int)rank * 128 + 32 * quarter, row = row0 + lane;
-      const float a_scale = row < p.rows ? p.a_scale[row] : 0.f;
-      for (int c = 0; c < per; c += kCols) {
-        const int col0 = tn * p.n_tile + part * per + c;
-        const int width = min(kCols, per - c);
-#pragma unroll
-        for (int h = 0; h < kCols; h += 32) {
-          if (h >= width) break;
+      // (rolled: a tile of a small product runs through here once, and instructions that are read once
+      // cost more than the rest)
+#pragma unroll 1
+      for (int c = 0; c < per; c += 32, col += 32) {
+        float w_next[4];
+        load_scales(w_next, p.w_scale, col + 32, end, p.vec);
+        {
           uint32_t r[32];
-          tmem_ld32_sync(lanes | (tmem + 256 * as + part * per + c + h), r);
-          float v[32];
+          tmem_ld32_sync(lanes | (tmem + 256 * as + first + c), r);
+          if (c + 32 >= per) {   // the accumulator is free
+            tc_fence_before();
+            if (lane == 0) mbar_arrive_remote(map_to_rank(acc_empty + 8 * as, 0));
+          }
+          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float4 w;
-            if (col0 + h + j + 3 < p.n) {
-              w = make_float4(p.w_scale[col0 + h + j], p.w_scale[col0 + h + j + 1], p.w_scale[col0 + h + j + 2],
-                              p.w_scale[col0 + h + j + 3]);
-            } else {
-              w.x = col0 + h + j < p.n ? p.w_scale[col0 + h + j] : 0.f;
-              w.y = col0 + h + j + 1 < p.n ? p.w_scale[col0 + h + j + 1] : 0.f;
-              w.z = col0 + h + j + 2 < p.n ? p.w_scale[col0 + h + j + 2] : 0.f;
-              w.w = 0.f;
+          for (int u = 0; u < 8; ++u)
+            st_shared_v4(box + lane * 128 + ((u ^ (lane & 7)) << 4), r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+          __syncwarp();
+        }
+        const uint8_t* from = smem + (box - sbase);
+        if (p.vec) {
+          OT* out = static_cast<OT*>(p.out) + (int64_t)(row0 + (lane >> 3)) * p.out_stride + col;
+          int4 v[8];   // all reads before the first store: the compiler keeps their order
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 4 * i + (lane >> 3);
+            v[i] = *reinterpret_cast<const int4*>(from + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 4 * i + (lane >> 3);
+            const float a = __shfl_sync(0xffffffffu, a_scale, rr);
+            const float o[4] = {(float)v[i].x * w[0] * a, (float)v[i].y * w[1] * a, (float)v[i].z * w[2] * a,
+                                (float)v[i].w * w[3] * a};
+            if (row0 + rr < p.rows) store4(out + 4 * i * p.out_stride, o, end - col);
+          }
+        } else {
+          OT* out = static_cast<OT*>(p.out) + (int64_t)row0 * p.out_stride + col;
+#pragma unroll 1
+          for (int r0 = 0; r0 < 32; r0 += 8) {
+            int v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[i] = *reinterpret_cast<const int*>(from + (r0 + i) * 128 + (((lane >> 2) ^ i) << 4) + 4 * (lane & 3));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float a = __shfl_sync(0xffffffffu, a_scale, r0 + i);
+              if (row0 + r0 + i < p.rows && col < end) store1(out + (r0 + i) * p.out_stride, (float)v[i] * w[0] * a);
             }
-            v[j] = (float)(int32_t)r[j] * w.x * a_scale;
-            v[j + 1] = (float)(int32_t)r[j + 1] * w.y * a_scale;
-            v[j + 2] = (float)(int32_t)r[j + 2] * w.z * a_scale;
-            v[j + 3] = (float)(int32_t)r[j + 3] * w.w * a_scale;
-          }
-          // 16-byte units of row `lane`, swizzled so that both directions are free of conflicts
-          constexpr int kUnits = 32 * (int)sizeof(OT) / 16;
-#pragma unroll
-          for (int u = 0; u < kUnits; ++u) {
-            const uint32_t at = box + lane * 128 + (((h * (int)sizeof(OT) / 16 + u) ^ (lane & 7)) << 4);
-            if constexpr (sizeof(OT) == 2)
-              st_shared_v4(at, pack_bf16(v[8 * u], v[8 * u + 1]), pack_bf16(v[8 * u + 2], v[8 * u + 3]),
-                           pack_bf16(v[8 * u + 4], v[8 * u + 5]), pack_bf16(v[8 * u + 6], v[8 * u + 7]));
-            else
-              st_shared_v4(at, __float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
-                           __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
           }
         }
-        __syncwarp();
-        const int unit = lane & 7, col = col0 + unit * (16 / (int)sizeof(OT));
-        const bool mine = unit * (16 / (int)sizeof(OT)) < width;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = 4 * i + (lane >> 3);
-          if (row0 + rr >= p.rows || !mine) continue;
-          const uint4 q = *reinterpret_cast<const uint4*>(smem + (box - sbase) + rr * 128 + ((unit ^ (rr & 7)) << 4));
-          OT* o = static_cast<OT*>(p.out) + (int64_t)(row0 + rr) * p.out_stride + col;
-          if (p.vec && col + 16 / (int)sizeof(OT) <= p.n) {
-            *reinterpret_cast<uint4*>(o) = q;
-          } else {
-            const OT* e = reinterpret_cast<const OT*>(&q);
-#pragma unroll
-            for (int j = 0; j < 16 / (int)sizeof(OT); ++j)
-              if (col + j < p.n) o[j] = e[j];
-          }
-        }
-        __syncwarp();
+        for (int j = 0; j < 4; ++j) w[j] = w_next[j];
       }
-      tc_fence_before();
-      if (lane == 0) mbar_arrive_remote(map_to_rank(acc_empty + 8 * as, 0));
     }
   }
   __syncwarp();
@@ -419,86 +499,150 @@ bool encode(CUtensorMap* m, const int8_t* base, uint64_t rows, uint64_t k, uint6
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// cudaFuncSetAttribute acts on the current device: once for each (a second call does no harm).
-template <auto kKernel>
-cudaError_t allow_smem(int device, uint32_t bytes) {
-  static std::atomic<uint64_t> done{0};
-  const uint64_t bit = device < 64 ? 1ull << device : 0;
-  if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
-}
+constexpr uint32_t kFewSmem = 113 * 1024, kFewSmemOne = 227 * 1024;   // two CTAs per SM, or one
 
-constexpr uint32_t kFewSmem = 108 * 1024;   // two CTAs per SM
+// How linear_few cuts its work: the CTAs that share a tile's sum, and the stages of their rings.
+struct FewShape {
+  int splits, stages;
+  uint32_t ring, smem;
+};
+FewShape few_shape(const mla_decode_s& h, int tiles, int kblocks, int n_tile) {
+  const uint32_t stage = kWBox + (uint32_t)n_tile * kBoxK;
+  FewShape best{};
+  int64_t least = INT64_MAX;
+  for (int splits = 1; splits <= kMaxSplits && (splits == 1 || kblocks >= 2 * splits); ++splits)
+    for (const bool two : {false, true}) {
+      const uint32_t channels = (128 + splits - 1) / splits;   // of a CTA, at most
+      const uint32_t parts = splits == 1 ? 0 : splits * channels * (((uint32_t)n_tile / 4) | 1) * 16;
+      const int per = (kblocks + splits - 1) / splits;
+      const uint32_t limit = two ? kFewSmem : kFewSmemOne;
+      if (limit < parts + 2048 + stage) continue;
+      FewShape f{};
+      f.splits = splits;
+      f.stages = std::min({kMaxFewStages, (int)((limit - parts - 2048) / stage), per});
+      if (f.stages < std::min(3, per)) continue;
+      f.ring = f.stages * stage;
+      f.smem = 2048 + f.ring + parts;
+      // In units of a k block's time: what an SM has to take, as often as not all clusters fit at once
+      // (two CTAs on an SM slow each other down), and what a wave and the exchange cost beside it.
+      const int clusters = h.few_clusters[f.smem <= kFewSmem][splits];
+      if (clusters < 1) continue;
+      const int64_t waves = (tiles + clusters - 1) / clusters;
+      const int64_t cost = waves * (10 * per * (tiles * splits > h.num_sms && f.smem <= kFewSmem ? 18 : 10) / 10 + 80) +
+                           (splits > 1 ? 20 : 0);
+      if (cost < least) {
+        least = cost;
+        best = f;
+      }
+    }
+  return best;
+}
 
 template <typename OT>
 cudaError_t launch_few(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s) {
-  const int n_tile = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 64 ? 64 : 128;
-  const int kblocks = (a.k + kBoxK - 1) / kBoxK;
-  const int blocks = (a.n + 127) / 128, row_tiles = (a.rows + n_tile - 1) / n_tile;
-  const uint32_t stage = kWBox + (uint32_t)n_tile * kBoxK;
-  int splits = 1;
-  while (splits < kMaxSplits && blocks * row_tiles * splits < h.num_sms && kblocks >= 4 * splits) splits *= 2;
-  const int stages = std::min((int)((kFewSmem - 2048) / stage), std::max((kblocks + splits - 1) / splits, 1));
-  // the ring also holds the partial tile
-  const uint32_t ring = std::max(stages * stage, (uint32_t)n_tile * 512);
-  const uint32_t smem = ring + 16 * stages + 64 + 1024;
-  CUtensorMap tw, ta;
-  if (!encode(&tw, a.w_codes, (uint64_t)a.n, (uint64_t)a.k, (uint64_t)a.w_stride, 128) ||
-      !encode(&ta, a.codes, (uint64_t)a.rows, (uint64_t)a.k, (uint64_t)a.codes_stride, (uint32_t)n_tile))
-    return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem<linear_few<OT>>(h.device, kFewSmem);
-  if (e != cudaSuccess) return e;
   FewParams p{};
   p.rows = a.rows;
   p.n = a.n;
-  p.n_tile = n_tile;
-  p.splits = splits;
-  p.kblocks = kblocks;
-  p.stages = stages;
-  p.ring = ring;
-  p.idesc = idesc_i8_s32(128, n_tile);
+  p.n_tile = (a.rows + 15) / 16 * 16;
+  p.kblocks = (a.k + kBoxK - 1) / kBoxK;
+  const int blocks = (a.n + 127) / 128;
+  const FewShape f = few_shape(h, blocks, p.kblocks, p.n_tile);
+  if (f.splits == 0) return cudaErrorInvalidValue;
+  p.splits = f.splits;
+  p.stages = f.stages;
+  p.ring = f.ring;
+  CUtensorMap tw, ta;
+  if (!encode(&tw, a.w_codes, (uint64_t)a.n, (uint64_t)a.k, (uint64_t)a.w_stride, 128) ||
+      !encode(&ta, a.codes, (uint64_t)a.rows, (uint64_t)a.k, (uint64_t)a.codes_stride, (uint32_t)p.n_tile))
+    return cudaErrorInvalidValue;
+  p.idesc = idesc_i8_s32(128, p.n_tile);
+  p.a_scale = a.scales;
+  p.w_scale = a.w_scales;
+  p.out = a.out;
+  p.out_stride = a.out_stride;
+  p.err = h.ws.err;
+  return launch_pdl_cluster(linear_few<OT>, dim3(blocks * p.splits), dim3(256), f.smem, p.splits, s, tw, ta, p);
+}
+
+// The channels per tile: the pairs work in rounds, a tile each, so what a round takes counts as often
+// as there are rounds.
+int many_tile(const LinearArgs& a, int clusters) {
+  const int64_t kblocks = (a.k + kBoxK - 1) / kBoxK, tiles_m = (a.rows + 255) / 256;
+  int best = 256;
+  int64_t least = INT64_MAX;
+  for (int tile = 256; tile >= 32; tile -= 32) {
+    const int64_t tiles = tiles_m * ((a.n + tile - 1) / tile), rounds = (tiles + clusters - 1) / clusters;
+    // cycles, as measured: a k block of a tile (2 x tile of them are the MMAs' at tile 256; narrower tiles
+    // read as many tokens for less), and the last tile's 32-column blocks on their way out
+    const int64_t cost = rounds * kblocks * (220 + 14 * tile / 10) + (tile + 63) / 64 * 900;
+    if (cost < least) {
+      least = cost;
+      best = tile;
+    }
+  }
+  return best;
+}
+
+template <typename OT>
+cudaError_t launch_many(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s) {
+  ManyParams p{};
+  p.rows = a.rows;
+  p.n = a.n;
+  p.kblocks = (a.k + kBoxK - 1) / kBoxK;
+  p.tiles_m = (a.rows + 255) / 256;
+  p.n_tile = many_tile(a, h.num_sms / 2);
+  p.tiles_n = (a.n + p.n_tile - 1) / p.n_tile;
+  p.group = 8;
+  p.stages = std::min<int>(kMaxManyStages, kManyRing / (kWBox + p.n_tile / 2 * kBoxK));
+  p.idesc = idesc_i8_s32(256, p.n_tile);
   p.a_scale = a.scales;
   p.w_scale = a.w_scales;
   p.out = a.out;
   p.out_stride = a.out_stride;
   p.vec = reinterpret_cast<uintptr_t>(a.out) % (4 * sizeof(OT)) == 0 && a.out_stride % 4 == 0;
   p.err = h.ws.err;
-  return launch_pdl_cluster(linear_few<OT>, dim3(blocks * splits, row_tiles), dim3(256), smem, splits, s, tw, ta, p);
-}
-
-template <typename OT>
-cudaError_t launch_many(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s) {
-  ManyParams p{};
-  p.n_tile = 256;
-  p.rows = a.rows;
-  p.n = a.n;
-  p.kblocks = (a.k + kBoxK - 1) / kBoxK;
-  p.tiles_m = (a.rows + 255) / 256;
-  p.tiles_n = (a.n + p.n_tile - 1) / p.n_tile;
-  p.group = 8;
-  p.idesc = idesc_i8_s32(256, p.n_tile);
-  p.a_scale = a.scales;
-  p.w_scale = a.w_scales;
-  p.out = a.out;
-  p.out_stride = a.out_stride;
-  p.vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride * sizeof(OT) % 16 == 0;
-  p.err = h.ws.err;
   CUtensorMap tw, ta;
   if (!encode(&tw, a.w_codes, (uint64_t)a.n, (uint64_t)a.k, (uint64_t)a.w_stride, (uint32_t)p.n_tile / 2) ||
       !encode(&ta, a.codes, (uint64_t)a.rows, (uint64_t)a.k, (uint64_t)a.codes_stride, 128))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem<linear_many<OT>>(h.device, kManySmem);
-  if (e != cudaSuccess) return e;
   const int clusters = std::min(h.num_sms / 2, p.tiles_m * p.tiles_n);
   return launch_pdl(linear_many<OT>, dim3(2 * clusters), dim3(kManyThreads), kManySmem, s, tw, ta, p);
 }
 
 }  // namespace
 
+cudaError_t init_linear_q8(mla_decode_s& h) {
+  const struct { const void* kernel; uint32_t smem; } need[] = {
+      {reinterpret_cast<const void*>(linear_few<float>), kFewSmemOne},
+      {reinterpret_cast<const void*>(linear_few<__nv_bfloat16>), kFewSmemOne},
+      {reinterpret_cast<const void*>(linear_many<float>), kManySmem},
+      {reinterpret_cast<const void*>(linear_many<__nv_bfloat16>), kManySmem}};
+  for (const auto& k : need) {
+    const cudaError_t e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
+    if (e != cudaSuccess) return e;
+  }
+  // a cluster stays within a group of SMs, so how many fit depends on the groups' sizes
+  for (const bool two : {false, true})
+    for (int splits = 1; splits <= kMaxSplits; ++splits) {
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = splits;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(splits);
+      cfg.blockDim = dim3(256);
+      cfg.dynamicSmemBytes = two ? kFewSmem : kFewSmemOne;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&h.few_clusters[two][splits], linear_few<float>, &cfg);
+      if (e != cudaSuccess) return e;
+    }
+  return cudaSuccess;
+}
+
 cudaError_t launch_linear_q8(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s) {
-  if (a.rows <= 128) return a.out_f32 ? launch_few<float>(h, a, s) : launch_few<__nv_bfloat16>(h, a, s);
+  if (a.rows <= kFewRows) return a.out_f32 ? launch_few<float>(h, a, s) : launch_few<__nv_bfloat16>(h, a, s);
   return a.out_f32 ? launch_many<float>(h, a, s) : launch_many<__nv_bfloat16>(h, a, s);
 }
 

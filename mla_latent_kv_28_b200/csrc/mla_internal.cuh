@@ -21,6 +21,7 @@ constexpr int kMaxTokenRows = 8192;  // (sequence, new token) rows per call: max
 constexpr int kMaxBatch = 1024;
 constexpr int kTileTokens = 64;  // tokens per KV tile: the unit of the work plan
 constexpr int kMaxNormWidth = 16384;      // add_norm_q8, quantize_rows: 16 values per thread of a block
+constexpr int kMaxSplits = 8;             // linear_q8: CTAs that share a sum (the portable cluster size)
 constexpr int kMaxLinearK = 131071;       // linear_q8: |sum| <= 2^14 k stays below 2^31
 constexpr int kMaxLinearRows = 1 << 20;   // ... rows and output channels
 constexpr int64_t kMaxLinearStride = (int64_t)1 << 32;   // ... bytes between rows (below TMA's 2^40)
@@ -72,6 +73,7 @@ struct mla_decode_s {
   int n_rows = 0;   // attention rows per sequence: n_heads * q_len (token-major)
   int group_rows = 0;   // rows per decode launch (the MMA's M = 128 at most); n_rows in groups
   double theta[mla::kDRope / 2] = {};  // RoPE pair frequencies (0: no rotation), YaRN applied
+  int few_clusters[2][mla::kMaxSplits + 1] = {};   // linear_q8: clusters that fit at once, [two CTAs per SM][CTAs]
   int units = 0;  // units the balanced plan cuts the tile space into
   mla::Workspace ws;
 };
@@ -231,6 +233,7 @@ struct LinearArgs {
   bool out_f32;
   int64_t out_stride;
 };
+cudaError_t init_linear_q8(mla_decode_s& h);   // once per handle, on its device
 cudaError_t launch_linear_q8(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s);
 
 // The cache rows of n_rows projected rows x [n_rows, 576] (cv.kv_exp != nullptr: E4M3 codes at c_kv).

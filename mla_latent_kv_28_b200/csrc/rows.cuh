@@ -130,6 +130,9 @@ __device__ __forceinline__ void store_pairs(__nv_bfloat16* p, int step, int left
       *q = __float2bfloat16_rn(c & 1 ? v[c >> 1].y : v[c >> 1].x);
   }
 }
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+
 template <typename T>
 __device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll

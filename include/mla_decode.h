@@ -326,8 +326,8 @@ MLA_API int mla_append_kv_fp8(mla_handle_t h, int32_t batch, int32_t d_model, co
  *   mla_add_norm_q8 -> mla_linear_q8 with [W^DQ ; W^DKV ; W^KR] -> mla_add_norm_q8 on the W^DQ
  *   columns (no residual) -> mla_linear_q8 with W^UQ and with W^QR; mla_append_rows on the other
  *   576 columns; mla_decode_step; mla_quantize_rows -> mla_linear_q8 with W^O.
- * These five calls use the handle's device whichever device is current, and no workspace: several
- * may run at once. Rows may lie apart (a stride in elements between rows, at least the row's
+ * These calls take their arguments as a struct (read before the call returns) and use the handle's
+ * device whichever device is current, and no workspace: several may run at once. Rows may lie apart (a stride in elements between rows, at least the row's
  * length); where a call says nothing else a pointer needs its elements' alignment only. n_rows 0
  * is valid and does nothing. Outputs must not overlap inputs, but for those named.
  */
@@ -358,19 +358,44 @@ enum {
  * Errors: MLA_ERR_INVALID_ARG for NULL pointers, a bad type, size, stride, rms_eps or alignment;
  * MLA_ERR_UNSUPPORTED for d > 16384 or n_rows >= 2^31.
  */
-MLA_API int mla_add_norm_q8(mla_handle_t h, int64_t n_rows, int32_t d, const void* x, int32_t x_type,
-                    int64_t x_stride, const void* residual, int64_t residual_stride, void* residual_out,
-                    int64_t residual_out_stride, int32_t residual_type, const void* gamma, float rms_eps,
-                    void* y, int64_t y_stride, int8_t* codes, int64_t codes_stride, float* scales,
-                    mla_stream_t stream);
+typedef struct {
+  int64_t n_rows;
+  int32_t d;
+  int32_t x_type;
+  const void* x;
+  int64_t x_stride;
+  const void* residual;
+  int64_t residual_stride;
+  void* residual_out;
+  int64_t residual_out_stride;
+  const void* gamma;
+  void* y;
+  int64_t y_stride;
+  int8_t* codes;
+  int64_t codes_stride;
+  float* scales;
+  int32_t residual_type;
+  float rms_eps;
+} mla_add_norm_q8_t;
+
+MLA_API int mla_add_norm_q8(mla_handle_t h, const mla_add_norm_q8_t* args, mla_stream_t stream);
 
 /*
  * The codes and scales of x itself (as above with t = x and rstd = 1): the heads' outputs on their
  * way into W^O, or a weight [n, k], whose rows are output channels. Errors as for mla_add_norm_q8.
  */
-MLA_API int mla_quantize_rows(mla_handle_t h, int64_t n_rows, int32_t d, const void* x, int32_t x_type,
-                    int64_t x_stride, int8_t* codes, int64_t codes_stride, float* scales,
-                    mla_stream_t stream);
+typedef struct {
+  int64_t n_rows;
+  int32_t d;
+  int32_t x_type;
+  const void* x;
+  int64_t x_stride;
+  int8_t* codes;
+  int64_t codes_stride;
+  float* scales;
+} mla_quantize_rows_t;
+
+MLA_API int mla_quantize_rows(mla_handle_t h, const mla_quantize_rows_t* args, mla_stream_t stream);
 
 /*
  * The product of int8 rows and an int8 weight, with a scale per row and per output channel:
@@ -386,10 +411,22 @@ MLA_API int mla_quantize_rows(mla_handle_t h, int64_t n_rows, int32_t d, const v
  * Errors: MLA_ERR_INVALID_ARG for NULL pointers, a bad type, size, stride or alignment;
  * MLA_ERR_UNSUPPORTED beyond the limits above or for strides over 2^32.
  */
-MLA_API int mla_linear_q8(mla_handle_t h, int32_t n_rows, int32_t k, int32_t n, const int8_t* codes,
-                    int64_t codes_stride, const float* scales, const int8_t* w_codes, int64_t w_stride,
-                    const float* w_scales, void* out, int32_t out_type, int64_t out_stride,
-                    mla_stream_t stream);
+typedef struct {
+  int32_t n_rows;
+  int32_t k;
+  int32_t n;
+  int32_t out_type;
+  const int8_t* codes;
+  int64_t codes_stride;
+  const float* scales;
+  const int8_t* w_codes;
+  int64_t w_stride;
+  const float* w_scales;
+  void* out;
+  int64_t out_stride;
+} mla_linear_q8_t;
+
+MLA_API int mla_linear_q8(mla_handle_t h, const mla_linear_q8_t* args, mla_stream_t stream);
 
 /*
  * mla_append_kv for rows that are projected already, x = [W_DKV ; W_KR] h (576 values):
@@ -409,21 +446,33 @@ MLA_API int mla_linear_q8(mla_handle_t h, int32_t n_rows, int32_t k, int32_t n, 
  * entry is outside 0..num_pages-1, sets the device error word and is skipped; the other rows are
  * written. Errors: MLA_ERR_INVALID_ARG as for mla_append_kv, and for a bad x_type or x_stride.
  */
-MLA_API int mla_append_rows(mla_handle_t h, int32_t batch, int32_t n_rows, const void* x, int32_t x_type,
-                    int64_t x_stride, const void* gamma, float rms_eps, void* c_kv, void* k_r,
-                    int64_t row_stride, int64_t seq_stride, const int32_t* kv_lens,
-                    const int32_t* row_starts, const int32_t* page_table, int32_t max_pages,
-                    int32_t num_pages, mla_stream_t stream);
+typedef struct {
+  int32_t batch;
+  int32_t n_rows;
+  int32_t x_type;
+  float rms_eps;
+  const void* x;
+  int64_t x_stride;
+  const void* gamma;
+  void* c_kv;            /* mla_append_rows_fp8: the codes */
+  void* k_r;             /* mla_append_rows_fp8: not read  */
+  int8_t* kv_exp;        /* mla_append_rows: not read      */
+  int64_t row_stride;
+  int64_t seq_stride;
+  const int32_t* kv_lens;
+  const int32_t* row_starts;
+  const int32_t* page_table;
+  int32_t max_pages;
+  int32_t num_pages;
+} mla_append_rows_t;
+
+MLA_API int mla_append_rows(mla_handle_t h, const mla_append_rows_t* args, mla_stream_t stream);
 
 /*
  * mla_append_rows into a quantised cache (codes and exponents as mla_append_kv_fp8 writes them: the
  * smallest power of two with max|row| / 2^e <= 448, values rounded to the nearest E4M3 code).
  */
-MLA_API int mla_append_rows_fp8(mla_handle_t h, int32_t batch, int32_t n_rows, const void* x, int32_t x_type,
-                    int64_t x_stride, const void* gamma, float rms_eps, void* kv_codes, int8_t* kv_exp,
-                    int64_t row_stride, int64_t seq_stride, const int32_t* kv_lens,
-                    const int32_t* row_starts, const int32_t* page_table, int32_t max_pages,
-                    int32_t num_pages, mla_stream_t stream);
+MLA_API int mla_append_rows_fp8(mla_handle_t h, const mla_append_rows_t* args, mla_stream_t stream);
 
 /*
  * mla_decode_attn for callers that cannot allocate device memory. The pages have no

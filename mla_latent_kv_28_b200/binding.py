@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -79,20 +80,21 @@ SIGNATURES = {
     "mla_merge_partials": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _P, _P]),
     "mla_append_kv": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _P, ctypes.c_float, _P, _P,
                                      _I64, _I64, _P, _P, _I32, _I32, _P]),
-    "mla_add_norm_q8": (ctypes.c_int, [_P, _I64, _I32, _P, _I32, _I64, _P, _I64, _P, _I64, _I32, _P,
-                                       ctypes.c_float, _P, _I64, _P, _I64, _P, _P]),
-    "mla_quantize_rows": (ctypes.c_int, [_P, _I64, _I32, _P, _I32, _I64, _P, _I64, _P, _P]),
-    "mla_linear_q8": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _I64, _P, _P, _I64, _P, _P, _I32, _I64, _P]),
-    "mla_append_rows": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _I64, _P, ctypes.c_float, _P, _P, _I64, _I64,
-                                       _P, _P, _P, _I32, _I32, _P]),
-    "mla_append_rows_fp8": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _I64, _P, ctypes.c_float, _P, _P, _I64,
-                                           _I64, _P, _P, _P, _I32, _I32, _P]),
+    **{name: (ctypes.c_int, [_P, ctypes.c_char_p, _P]) for name in (
+        "mla_add_norm_q8", "mla_quantize_rows", "mla_linear_q8", "mla_append_rows", "mla_append_rows_fp8")},
     "mla_decode_attn_noalloc": (ctypes.c_int, [_I32, ctypes.c_float, _I32, _I64, _I32, _P, _P, _P,
                                                _I64, _I64, _P, _P, _I32, _I32, _P, _P, _P, _P]),
     "mla_check_device_errors": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "mla_workspace_bytes": (ctypes.c_int64, [_P]),
     "mla_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
+
+# The argument structs of the calls around the decode step (mla_add_norm_q8_t and so on), packed into
+# bytes: a fraction of what passing each argument by itself takes.
+NORM_ARGS = struct.Struct("qiiQqQqQqQQqQqQif")
+QUANTIZE_ARGS = struct.Struct("qiiQqQqQ")
+LINEAR_ARGS = struct.Struct("iiiiQqQQqQQq")
+ROWS_ARGS = struct.Struct("iiifQqQQQQqqQQQii")
 
 _lib = None
 
@@ -521,12 +523,12 @@ class MlaDecode:
         elif want_y:
             y, y_stride = torch.empty_strided(shape, (d, 1), dtype=torch.bfloat16, device=device), d
         if rows > 0:
-            _check(self._lib.mla_add_norm_q8(
-                self._h, rows, d, x.data_ptr(), ROW_TYPES[x.dtype], x_stride,
-                None if residual is None else residual.data_ptr(), res_stride,
-                None if residual is None else residual_out.data_ptr(), out_stride, res_type, gamma.data_ptr(), eps,
-                None if y is None else y.data_ptr(), y_stride, codes.data_ptr(), codes_stride, scales.data_ptr(),
-                self._here(stream)), "mla_add_norm_q8")
+            args = NORM_ARGS.pack(
+                rows, d, ROW_TYPES[x.dtype], x.data_ptr(), x_stride, 0 if residual is None else residual.data_ptr(),
+                res_stride, 0 if residual is None else residual_out.data_ptr(), out_stride, gamma.data_ptr(),
+                0 if y is None else y.data_ptr(), y_stride, codes.data_ptr(), codes_stride, scales.data_ptr(),
+                res_type, eps)
+            _check(self._lib.mla_add_norm_q8(self._h, args, self._here(stream)), "mla_add_norm_q8")
         return codes, scales, residual_out, y
 
     def quantize_rows(self, x: torch.Tensor, codes: Optional[torch.Tensor] = None,
@@ -537,9 +539,9 @@ class MlaDecode:
         rows, d = x.shape
         codes, codes_stride, scales = self._new_codes(rows, d, codes, scales, x.device)
         if rows > 0:
-            _check(self._lib.mla_quantize_rows(
-                self._h, rows, d, x.data_ptr(), ROW_TYPES[x.dtype], x_stride, codes.data_ptr(), codes_stride,
-                scales.data_ptr(), self._here(stream)), "mla_quantize_rows")
+            args = QUANTIZE_ARGS.pack(rows, d, ROW_TYPES[x.dtype], x.data_ptr(), x_stride, codes.data_ptr(),
+                                      codes_stride, scales.data_ptr())
+            _check(self._lib.mla_quantize_rows(self._h, args, self._here(stream)), "mla_quantize_rows")
         return codes, scales
 
     def linear_q8(self, codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
@@ -568,14 +570,13 @@ class MlaDecode:
         if n == 1:
             w_stride = (k + 15) // 16 * 16
         if rows > 0:
-            _check(self._lib.mla_linear_q8(
-                self._h, rows, k, n, codes.data_ptr(), a_stride, scales.data_ptr(), w_codes.data_ptr(), w_stride,
-                w_scales.data_ptr(), out.data_ptr(), ROW_TYPES[out_dtype], out_stride, self._here(stream)),
-                "mla_linear_q8")
+            args = LINEAR_ARGS.pack(rows, k, n, ROW_TYPES[out_dtype], codes.data_ptr(), a_stride, scales.data_ptr(),
+                                    w_codes.data_ptr(), w_stride, w_scales.data_ptr(), out.data_ptr(), out_stride)
+            _check(self._lib.mla_linear_q8(self._h, args, self._here(stream)), "mla_linear_q8")
         return out
 
-    def _append_rows_args(self, x, gamma, cache, cache_type, kv_lens, row_starts, page_table):
-        """The checked arguments that append_rows and append_rows_fp8 share."""
+    def _append_rows(self, call, x, gamma, cache, cache_type, exps, kv_lens, row_starts, page_table, eps, stream):
+        """The checks and the call that append_rows and append_rows_fp8 share (exps: a quantised cache)."""
         x_stride = self._rows(x, "x", ROW_TYPES)
         if x.shape[1] != ROW:
             raise ValueError(f"x: expected [rows, {ROW}], got {_shape(x)}")
@@ -596,14 +597,31 @@ class MlaDecode:
                     sizes[1] < self.cfg.max_kv_len:
                 raise ValueError(f"cache: expected [>= {B}, >= {self.cfg.max_kv_len}, {ROW}] with a whole number of "
                                  f"rows between sequences, got {_shape(cache)}")
-            return B, x_stride, row_stride, max(seq_stride, sizes[1]), 0, 0
-        if page_table.get_device() != self.device or page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+            seq_stride, max_pages, num_pages = max(seq_stride, sizes[1]), 0, 0
+        elif page_table.get_device() != self.device or page_table.dtype != torch.int32 or page_table.dim() != 2 or \
                 page_table.shape[0] < B or not page_table.is_contiguous():
             raise ValueError(f"page_table: expected a contiguous int32 [>= {B}, pages] tensor on "
                              f"cuda:{self.device}, got {_shape(page_table)}")
-        if sizes[1] != self.cfg.page_size or (sizes[0] > 1 and strides[0] != sizes[1] * row_stride):
+        elif sizes[1] != self.cfg.page_size or (sizes[0] > 1 and strides[0] != sizes[1] * row_stride):
             raise ValueError(f"cache: expected pages of {self.cfg.page_size} rows end to end, got {_shape(cache)}")
-        return B, x_stride, row_stride, 0, page_table.shape[1], sizes[0]
+        else:
+            seq_stride, max_pages, num_pages = 0, page_table.shape[1], sizes[0]
+        c_kv = cache.data_ptr()
+        if exps is None:
+            k_r, kv_exp = c_kv + 2 * D_LATENT, 0
+        else:
+            if exps.get_device() != self.device or exps.dtype != torch.int8 or exps.shape != sizes[:2] or \
+                    not exps.is_contiguous() or (page_table is None and seq_stride != sizes[1]):
+                raise ValueError(f"exps: expected a contiguous int8 {tuple(sizes[:2])} tensor indexed as codes is, "
+                                 f"got {_shape(exps)}")
+            k_r, kv_exp = 0, exps.data_ptr()
+        rows = x.shape[0]
+        if rows > 0:
+            args = ROWS_ARGS.pack(B, rows, ROW_TYPES[x.dtype], eps, x.data_ptr(), x_stride, gamma.data_ptr(), c_kv, k_r,
+                                  kv_exp, row_stride, seq_stride, kv_lens.data_ptr(),
+                                  0 if row_starts is None else row_starts.data_ptr(),
+                                  0 if page_table is None else page_table.data_ptr(), max_pages, num_pages)
+            _check(getattr(self._lib, call)(self._h, args, self._here(stream)), call)
 
     def append_rows(self, x: torch.Tensor, gamma: torch.Tensor, cache: torch.Tensor, kv_lens: torch.Tensor,
                     row_starts: Optional[torch.Tensor] = None, page_table: Optional[torch.Tensor] = None,
@@ -612,35 +630,16 @@ class MlaDecode:
         [rows, 576] (bf16 or fp32; rows may lie apart): rows row_starts[b] .. row_starts[b+1]-1 are
         the last of sequence b's kv_lens[b] tokens; without row_starts every sequence has q_len.
         Rows outside every sequence write nothing. cache as for decode_attn; returned."""
-        B, x_stride, row_stride, seq_stride, max_pages, num_pages = self._append_rows_args(
-            x, gamma, cache, torch.bfloat16, kv_lens, row_starts, page_table)
-        c_kv = cache.data_ptr()
-        if x.shape[0] > 0:
-            _check(self._lib.mla_append_rows(
-                self._h, B, x.shape[0], x.data_ptr(), ROW_TYPES[x.dtype], x_stride, gamma.data_ptr(), eps, c_kv,
-                c_kv + 2 * D_LATENT, row_stride, seq_stride, kv_lens.data_ptr(),
-                None if row_starts is None else row_starts.data_ptr(),
-                None if page_table is None else page_table.data_ptr(), max_pages, num_pages, self._here(stream)),
-                "mla_append_rows")
+        self._append_rows("mla_append_rows", x, gamma, cache, torch.bfloat16, None, kv_lens, row_starts, page_table,
+                          eps, stream)
         return cache
 
     def append_rows_fp8(self, x: torch.Tensor, gamma: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
                         kv_lens: torch.Tensor, row_starts: Optional[torch.Tensor] = None,
                         page_table: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None):
         """append_rows into a quantised cache: codes uint8 and exps int8 as for decode_attn_fp8."""
-        B, x_stride, row_stride, seq_stride, max_pages, num_pages = self._append_rows_args(
-            x, gamma, codes, torch.uint8, kv_lens, row_starts, page_table)
-        if exps.get_device() != self.device or exps.dtype != torch.int8 or exps.shape != codes.shape[:2] or \
-                not exps.is_contiguous() or (page_table is None and seq_stride != codes.shape[1]):
-            raise ValueError(f"exps: expected a contiguous int8 {tuple(codes.shape[:2])} tensor indexed as codes is, "
-                             f"got {_shape(exps)}")
-        if x.shape[0] > 0:
-            _check(self._lib.mla_append_rows_fp8(
-                self._h, B, x.shape[0], x.data_ptr(), ROW_TYPES[x.dtype], x_stride, gamma.data_ptr(), eps,
-                codes.data_ptr(), exps.data_ptr(), row_stride, seq_stride, kv_lens.data_ptr(),
-                None if row_starts is None else row_starts.data_ptr(),
-                None if page_table is None else page_table.data_ptr(), max_pages, num_pages, self._here(stream)),
-                "mla_append_rows_fp8")
+        self._append_rows("mla_append_rows_fp8", x, gamma, codes, torch.uint8, exps, kv_lens, row_starts, page_table,
+                          eps, stream)
         return codes, exps
 
     def step(self, q_c, q_r, w_uk, w_uv, cache, kv_lens, page_table=None, stream=None,

@@ -539,133 +539,121 @@ int rows_q8_common(mla_handle_t h, const mla::NormArgs& a, int32_t x_type, int32
   return mla::launch_norm_q8(*h, a, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
-// The shared body of mla_append_rows (bf16 rows) and mla_append_rows_fp8 (kv_exp != nullptr:
-// E4M3 codes at c_kv, row_stride in bytes).
-int append_rows_common(mla_handle_t h, int32_t batch, int32_t n_rows, const void* x, int32_t x_type,
-                       int64_t x_stride, const void* gamma, float rms_eps, void* c_kv, void* k_r,
-                       int8_t* kv_exp, int64_t row_stride, int64_t seq_stride, const int32_t* kv_lens,
-                       const int32_t* row_starts, const int32_t* page_table, int32_t max_pages,
-                       int32_t num_pages, mla_stream_t stream) {
-  if (h == nullptr || x == nullptr || gamma == nullptr || c_kv == nullptr || k_r == nullptr || kv_lens == nullptr)
+// The shared body of mla_append_rows (bf16 rows) and mla_append_rows_fp8 (E4M3 codes at c_kv,
+// row_stride in bytes).
+int append_rows_common(mla_handle_t h, const mla_append_rows_t* a, bool fp8, mla_stream_t stream) {
+  if (h == nullptr || a == nullptr || a->x == nullptr || a->gamma == nullptr || a->c_kv == nullptr ||
+      (fp8 ? a->kv_exp == nullptr : a->k_r == nullptr) || a->kv_lens == nullptr)
     return MLA_ERR_INVALID_ARG;
-  if (batch < 1 || batch > h->cfg.max_batch || n_rows < 0) return MLA_ERR_INVALID_ARG;
-  if (row_starts == nullptr && n_rows != batch * h->q_len) return MLA_ERR_INVALID_ARG;
-  const int xb = type_bytes(x_type);
-  if (xb == 0 || x_stride < mla::kRow || x_stride * xb % 16 != 0 || !aligned16(x) || !aligned16(gamma))
+  if (a->batch < 1 || a->batch > h->cfg.max_batch || a->n_rows < 0) return MLA_ERR_INVALID_ARG;
+  if (a->row_starts == nullptr && a->n_rows != a->batch * h->q_len) return MLA_ERR_INVALID_ARG;
+  const int xb = type_bytes(a->x_type);
+  if (xb == 0 || a->x_stride < mla::kRow || a->x_stride * xb % 16 != 0 || !aligned16(a->x) || !aligned16(a->gamma))
     return MLA_ERR_INVALID_ARG;
-  if (!(rms_eps >= 0.f) || !std::isfinite(rms_eps)) return MLA_ERR_INVALID_ARG;
-  if (!aligned(kv_lens, 4) || !aligned(row_starts, 4) || !aligned(page_table, 4)) return MLA_ERR_INVALID_ARG;
-  if (kv_exp != nullptr && (row_stride < mla::kRow || row_stride % 16 != 0)) return MLA_ERR_INVALID_ARG;
+  if (!(a->rms_eps >= 0.f) || !std::isfinite(a->rms_eps)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(a->kv_lens, 4) || !aligned(a->row_starts, 4) || !aligned(a->page_table, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (fp8 && (a->row_stride < mla::kRow || a->row_stride % 16 != 0)) return MLA_ERR_INVALID_ARG;
+  void* k_r = fp8 ? a->c_kv : a->k_r;
   mla::CacheView cv{};
-  const int st = cache_view(h, c_kv, k_r, row_stride, seq_stride, page_table, max_pages, num_pages, &cv);
+  const int st = cache_view(h, a->c_kv, k_r, a->row_stride, a->seq_stride, a->page_table, a->max_pages,
+                            a->num_pages, &cv);
   if (st != MLA_OK) return st;
-  cv.kv_exp = kv_exp;
-  if (n_rows == 0) return MLA_OK;
+  if (fp8) cv.kv_exp = a->kv_exp;
+  if (a->n_rows == 0) return MLA_OK;
   const OnDevice on(h->device);
   if (!on.ok()) return MLA_ERR_CUDA;
   const cudaError_t e = mla::launch_append_rows(
-      *h, batch, n_rows, x, x_type == MLA_F32, x_stride, static_cast<const __nv_bfloat16*>(gamma), rms_eps, cv,
-      static_cast<__nv_bfloat16*>(c_kv), static_cast<__nv_bfloat16*>(k_r), kv_lens, row_starts, stream);
+      *h, a->batch, a->n_rows, a->x, a->x_type == MLA_F32, a->x_stride, static_cast<const __nv_bfloat16*>(a->gamma),
+      a->rms_eps, cv, static_cast<__nv_bfloat16*>(a->c_kv), static_cast<__nv_bfloat16*>(k_r), a->kv_lens,
+      a->row_starts, stream);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // namespace
 
-int mla_add_norm_q8(mla_handle_t h, int64_t n_rows, int32_t d, const void* x, int32_t x_type, int64_t x_stride,
-                    const void* residual, int64_t residual_stride, void* residual_out,
-                    int64_t residual_out_stride, int32_t residual_type, const void* gamma, float rms_eps,
-                    void* y, int64_t y_stride, int8_t* codes, int64_t codes_stride, float* scales,
-                    mla_stream_t stream) {
-  if (h == nullptr || x == nullptr || gamma == nullptr || (y == nullptr && codes == nullptr))
+int mla_add_norm_q8(mla_handle_t h, const mla_add_norm_q8_t* args, mla_stream_t stream) {
+  if (h == nullptr || args == nullptr || args->x == nullptr || args->gamma == nullptr ||
+      (args->y == nullptr && args->codes == nullptr))
     return MLA_ERR_INVALID_ARG;
-  if (!(rms_eps >= 0.f) || !std::isfinite(rms_eps)) return MLA_ERR_INVALID_ARG;
+  if (!(args->rms_eps >= 0.f) || !std::isfinite(args->rms_eps)) return MLA_ERR_INVALID_ARG;
   mla::NormArgs a{};
-  a.n_rows = n_rows;
-  a.d = d;
-  a.x = x;
-  a.x_f32 = x_type == MLA_F32;
-  a.x_stride = x_stride;
-  a.residual = residual;
-  a.residual_out = residual_out;
-  a.residual_f32 = residual_type == MLA_F32;
-  a.residual_stride = residual_stride;
-  a.residual_out_stride = residual_out_stride;
-  a.gamma = static_cast<const __nv_bfloat16*>(gamma);
-  a.eps = rms_eps;
-  a.y = static_cast<__nv_bfloat16*>(y);
-  a.y_stride = y_stride;
-  a.codes = codes;
-  a.codes_stride = codes_stride;
-  a.scales = scales;
-  return rows_q8_common(h, a, x_type, residual_type, stream);
+  a.n_rows = args->n_rows;
+  a.d = args->d;
+  a.x = args->x;
+  a.x_f32 = args->x_type == MLA_F32;
+  a.x_stride = args->x_stride;
+  a.residual = args->residual;
+  a.residual_out = args->residual_out;
+  a.residual_f32 = args->residual_type == MLA_F32;
+  a.residual_stride = args->residual_stride;
+  a.residual_out_stride = args->residual_out_stride;
+  a.gamma = static_cast<const __nv_bfloat16*>(args->gamma);
+  a.eps = args->rms_eps;
+  a.y = static_cast<__nv_bfloat16*>(args->y);
+  a.y_stride = args->y_stride;
+  a.codes = args->codes;
+  a.codes_stride = args->codes_stride;
+  a.scales = args->scales;
+  return rows_q8_common(h, a, args->x_type, args->residual_type, stream);
 }
 
-int mla_quantize_rows(mla_handle_t h, int64_t n_rows, int32_t d, const void* x, int32_t x_type, int64_t x_stride,
-                      int8_t* codes, int64_t codes_stride, float* scales, mla_stream_t stream) {
-  if (h == nullptr || x == nullptr || codes == nullptr || scales == nullptr) return MLA_ERR_INVALID_ARG;
+int mla_quantize_rows(mla_handle_t h, const mla_quantize_rows_t* args, mla_stream_t stream) {
+  if (h == nullptr || args == nullptr || args->x == nullptr || args->codes == nullptr || args->scales == nullptr)
+    return MLA_ERR_INVALID_ARG;
   mla::NormArgs a{};
-  a.n_rows = n_rows;
-  a.d = d;
-  a.x = x;
-  a.x_f32 = x_type == MLA_F32;
-  a.x_stride = x_stride;
-  a.codes = codes;
-  a.codes_stride = codes_stride;
-  a.scales = scales;
-  return rows_q8_common(h, a, x_type, MLA_BF16, stream);
+  a.n_rows = args->n_rows;
+  a.d = args->d;
+  a.x = args->x;
+  a.x_f32 = args->x_type == MLA_F32;
+  a.x_stride = args->x_stride;
+  a.codes = args->codes;
+  a.codes_stride = args->codes_stride;
+  a.scales = args->scales;
+  return rows_q8_common(h, a, args->x_type, MLA_BF16, stream);
 }
 
-int mla_linear_q8(mla_handle_t h, int32_t n_rows, int32_t k, int32_t n, const int8_t* codes, int64_t codes_stride,
-                  const float* scales, const int8_t* w_codes, int64_t w_stride, const float* w_scales, void* out,
-                  int32_t out_type, int64_t out_stride, mla_stream_t stream) {
-  if (h == nullptr || codes == nullptr || scales == nullptr || w_codes == nullptr || w_scales == nullptr ||
-      out == nullptr)
+int mla_linear_q8(mla_handle_t h, const mla_linear_q8_t* args, mla_stream_t stream) {
+  if (h == nullptr || args == nullptr || args->codes == nullptr || args->scales == nullptr ||
+      args->w_codes == nullptr || args->w_scales == nullptr || args->out == nullptr)
     return MLA_ERR_INVALID_ARG;
-  const int ob = type_bytes(out_type);
-  if (n_rows < 0 || k < 1 || n < 1 || ob == 0) return MLA_ERR_INVALID_ARG;
-  if (codes_stride < k || codes_stride % 16 != 0 || w_stride < k || w_stride % 16 != 0 || out_stride < n)
+  const int32_t rows = args->n_rows, k = args->k, n = args->n;
+  const int64_t codes_stride = args->codes_stride, w_stride = args->w_stride;
+  const int ob = type_bytes(args->out_type);
+  if (rows < 0 || k < 1 || n < 1 || ob == 0) return MLA_ERR_INVALID_ARG;
+  if (codes_stride < k || codes_stride % 16 != 0 || w_stride < k || w_stride % 16 != 0 || args->out_stride < n)
     return MLA_ERR_INVALID_ARG;
-  if (!aligned16(codes) || !aligned16(w_codes) || !aligned(scales, 4) || !aligned(w_scales, 4) ||
-      !aligned(out, ob))
+  if (!aligned16(args->codes) || !aligned16(args->w_codes) || !aligned(args->scales, 4) ||
+      !aligned(args->w_scales, 4) || !aligned(args->out, ob))
     return MLA_ERR_INVALID_ARG;
-  if (k > mla::kMaxLinearK || n_rows > mla::kMaxLinearRows || n > mla::kMaxLinearRows ||
+  if (k > mla::kMaxLinearK || rows > mla::kMaxLinearRows || n > mla::kMaxLinearRows ||
       codes_stride > mla::kMaxLinearStride || w_stride > mla::kMaxLinearStride)
     return MLA_ERR_UNSUPPORTED;
-  if (n_rows == 0) return MLA_OK;
+  if (rows == 0) return MLA_OK;
   const OnDevice on(h->device);
   if (!on.ok()) return MLA_ERR_CUDA;
   mla::LinearArgs a{};
-  a.rows = n_rows;
+  a.rows = rows;
   a.n = n;
   a.k = k;
-  a.codes = codes;
+  a.codes = args->codes;
   a.codes_stride = codes_stride;
-  a.scales = scales;
-  a.w_codes = w_codes;
+  a.scales = args->scales;
+  a.w_codes = args->w_codes;
   a.w_stride = w_stride;
-  a.w_scales = w_scales;
-  a.out = out;
-  a.out_f32 = out_type == MLA_F32;
-  a.out_stride = out_stride;
+  a.w_scales = args->w_scales;
+  a.out = args->out;
+  a.out_f32 = args->out_type == MLA_F32;
+  a.out_stride = args->out_stride;
   return mla::launch_linear_q8(*h, a, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
-int mla_append_rows(mla_handle_t h, int32_t batch, int32_t n_rows, const void* x, int32_t x_type, int64_t x_stride,
-                    const void* gamma, float rms_eps, void* c_kv, void* k_r, int64_t row_stride,
-                    int64_t seq_stride, const int32_t* kv_lens, const int32_t* row_starts,
-                    const int32_t* page_table, int32_t max_pages, int32_t num_pages, mla_stream_t stream) {
-  return append_rows_common(h, batch, n_rows, x, x_type, x_stride, gamma, rms_eps, c_kv, k_r, nullptr, row_stride,
-                            seq_stride, kv_lens, row_starts, page_table, max_pages, num_pages, stream);
+int mla_append_rows(mla_handle_t h, const mla_append_rows_t* args, mla_stream_t stream) {
+  return append_rows_common(h, args, false, stream);
 }
 
-int mla_append_rows_fp8(mla_handle_t h, int32_t batch, int32_t n_rows, const void* x, int32_t x_type,
-                        int64_t x_stride, const void* gamma, float rms_eps, void* kv_codes, int8_t* kv_exp,
-                        int64_t row_stride, int64_t seq_stride, const int32_t* kv_lens,
-                        const int32_t* row_starts, const int32_t* page_table, int32_t max_pages,
-                        int32_t num_pages, mla_stream_t stream) {
-  if (kv_exp == nullptr) return MLA_ERR_INVALID_ARG;
-  return append_rows_common(h, batch, n_rows, x, x_type, x_stride, gamma, rms_eps, kv_codes, kv_codes, kv_exp,
-                            row_stride, seq_stride, kv_lens, row_starts, page_table, max_pages, num_pages, stream);
+int mla_append_rows_fp8(mla_handle_t h, const mla_append_rows_t* args, mla_stream_t stream) {
+  return append_rows_common(h, args, true, stream);
 }
 
 int mla_check_device_errors(mla_handle_t h, mla_stream_t stream, uint32_t* detail) {

@@ -167,9 +167,8 @@ def test_eps_and_only_y(handle):
     x, g = rows_of(4, 384, BF, 14), gamma_of(384)
     check(handle, x, g, eps=0.7)
     y = torch.empty_like(x)
-    lib, s = handle._lib, torch.cuda.current_stream().cuda_stream
-    assert lib.mla_add_norm_q8(handle._h, 4, 384, x.data_ptr(), 0, 384, None, 0, None, 0, 0, g.data_ptr(), 1e-6,
-                               y.data_ptr(), 384, None, 0, None, s) == binding.MLA_OK
+    args = binding.NORM_ARGS.pack(4, 384, 0, x.data_ptr(), 384, 0, 0, 0, 0, g.data_ptr(), y.data_ptr(), 384, 0, 0, 0, 0, 1e-6)
+    assert handle._lib.mla_add_norm_q8(handle._h, args, torch.cuda.current_stream().cuda_stream) == binding.MLA_OK
     assert torch.equal(y, handle.add_norm_q8(x, g, want_y=True)[3])
 
 

@@ -11,17 +11,16 @@
 // depend on no sum: they are the nearest integers (ties to even) of 127 t / m for the fp32 t and m,
 // the same on every run and for every layout. The integer is first taken from t * (127 / m) in fp32,
 // off by the reciprocal's rounding, under 127 * 2^-24 = 7.6e-6; where the distance to it exceeds
-// 0.49998 the eight values are taken again from 127 t / m in fp64 (a quotient of a 31-bit by a
-// 24-bit number that is not on a border lies at least 2^-33 off it).
+// 0.49998 the side of the border is decided by 127 t - border * m, exact in fp64.
 //
 // A group of threads takes a row: 8, 16 or 32 lanes up to 1024 values, a block of its own beyond. A
 // thread holds NV vectors of 8 values of t (neighbours where rows are 16-byte aligned) and nothing
 // else across the reduction. Bound by HBM: per value the bytes of x, the residual in and out, one
-// code, and y where it is wanted; then by the issue slots (packed fp32 pairs and three-way maxima:
-// some 5 instructions per value without a norm). Measured: 4096 x 5120 bf16 with an fp32 residual
-// and y 42.5 us (6420 GB/s); 2048 x 16384 bf16 quantised 22.6 us (4450 GB/s, the codes' instructions
-// and the two phases of a row not fully hidden); one row of 5120 2.2 us, the launch and one round trip.
-// Rows of odd width (one value at a time) run at half to three quarters of that.
+// code, and y where it is wanted; rows of bf16 without a residual also by the issue slots (10
+// instructions per value with packed fp32 pairs and two- and three-way maxima). Measured: 4096 x 5120
+// bf16 with an fp32 residual and y 42.4 us (6430 GB/s); 2048 x 16384 bf16 quantised 19.8 us (5090 GB/s),
+// the same in fp32 26.3 us (6390 GB/s); one row of 5120 2.1 us, the launch and one round trip. Rows of odd
+// width (one value at a time) take up to three times as long in bf16 (4882 x 4095 36 against 13 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -86,30 +85,38 @@ struct Stats {
   }
 };
 
-// The integers nearest to 127 t / m, ties to even, the slow way.
-__device__ __noinline__ uint2 exact_codes(float2 a, float2 b, float2 c, float2 d, float m) {
-  const float t[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i >> 2] |= ((uint32_t)__double2int_rn((double)t[i] * 127.0 / (double)m) & 0xFFu) << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
+constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer in the low bits
+
+// The same integer for a value near the border between two, decided by the sign of 127 t - border * m
+// (24 + 8 bits each: exact in fp64), ties to even. k: kMagic + the nearest integer by fp32.
+__device__ __forceinline__ float at_border(float k, float t, float m, float inv) {
+  const float j = k - kMagic, e = fmaf(t, inv, -j);
+  if (!(fabsf(e) > 0.49998f)) return k;
+  const double over = fma(-(double)m, (double)(j + copysignf(0.5f, e)), (double)t * 127.0);
+  const bool odd = __float_as_uint(k) & 1u;
+  if (e > 0.f) return over > 0.0 || (over == 0.0 && odd) ? k + 1.f : k;
+  return over < 0.0 || (over == 0.0 && odd) ? k - 1.f : k;
 }
 
-// Eight codes; inv = 127 / m (0: a row of zeros).
+// Eight codes, the integers nearest to 127 t / m, ties to even; inv = 127 / m (0: a row of zeros).
 __device__ __forceinline__ uint2 codes8(const float2 (&t)[4], float m, float inv) {
-  constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer in the low bits
-  const float2 inv2 = make_float2(inv, inv), magic = make_float2(kMagic, kMagic);
+  const float2 inv2 = make_float2(inv, inv), magic = make_float2(kMagic, kMagic), minus = make_float2(-1.f, -1.f);
   float2 k[4];
   float off = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     k[i] = sm100::ffma2(t[i], inv2, magic);
-    const float2 j = sm100::fadd2(k[i], make_float2(-kMagic, -kMagic));
-    const float2 e = sm100::ffma2(t[i], inv2, make_float2(-j.x, -j.y));
+    const float2 j = sm100::ffma2(k[i], minus, magic);   // minus the integer
+    const float2 e = sm100::ffma2(t[i], inv2, j);
     off = max_abs(off, e.x, e.y);
   }
-  if (off > 0.49998f) return exact_codes(t[0], t[1], t[2], t[3], m);
+  if (off > 0.49998f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      k[i].x = at_border(k[i].x, t[i].x, m, inv);
+      k[i].y = at_border(k[i].y, t[i].y, m, inv);
+    }
+  }
   const auto pack = [](const float2& a, const float2& b) {
     return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
                        __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
@@ -150,11 +157,7 @@ norm_q8_kernel(const NormParams p) {
       rx[n].load(x + e, step, d - e);
     }
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) t[0][i] = rx[n].pair(i);
-      st.largest(t[0]);
-    }
+    for (int n = 0; n < NV; ++n) rx[n].largest(st.m);
   } else {
     Raw8<Res, W> rr[NV];
     Raw8<__nv_bfloat16, W> rg[NV];
@@ -242,13 +245,17 @@ norm_q8_kernel(const NormParams p) {
     }
     if (p.codes == nullptr) return;
   }
-  const float m = __uint_as_float(mb);
+  float m = __uint_as_float(mb);
   const bool finite = mb < 0x7F800000u;
   if (tid == 0 && d > 0)
     p.scales[row] = !finite ? __uint_as_float(0x7FC00000u) : m > 0.f ? m * rstd / 127.f : 0.f;
-  // below 1e-30, where 127 / m may overflow, every code is taken the slow way
-  const bool tiny = m > 0.f && m < 1e-30f;
-  const float inv = finite && m >= 1e-30f ? 127.f / m : 0.f;
+  // below 1e-30, where 127 / m may overflow, the row is scaled up by a power of two (exact)
+  float lift = 1.f;
+  if (m < 1e-30f) {
+    lift = 0x1p100f;
+    m *= lift;
+  }
+  const float inv = finite && m > 0.f ? 127.f / m : 0.f;
   int8_t* codes = p.codes + row * p.codes_stride;
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
@@ -259,7 +266,13 @@ norm_q8_kernel(const NormParams p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = rx[n].pair(i);
     }
-    if (finite) c = tiny ? exact_codes(v[0], v[1], v[2], v[3], m) : codes8(v, m, inv);
+    if (finite) {
+      if (lift != 1.f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = make_float2(v[i].x * lift, v[i].y * lift);
+      }
+      c = codes8(v, m, inv);
+    }
     store_codes<W>(codes + e, step, d - e, c);
   }
 }
@@ -314,15 +327,21 @@ cudaError_t launch_typed(const NormParams& p, int num_sms, cudaStream_t s) {
   if (p.d <= 512) return launch_shape<XT, RT, kNorm, 2, 8, 32>(p, s);
   if (p.d <= 768) return launch_shape<XT, RT, kNorm, 3, 8, 32>(p, s);
   if (p.d <= 1024) return launch_shape<XT, RT, kNorm, 4, 8, 32>(p, s);
+  // A little over 1024 values fill a block of their own badly: five vectors a lane where rows are many
+  // and no residual takes registers (16276 x 1232 bf16 quantised 13.2 against 18.1 us; with an fp32
+  // residual 35.1 against 34.3 us; 2048 values in eight vectors 15.3 against 12.8 us).
+  if constexpr (!kRes)
+    if (p.d <= 1280 && p.n_rows >= 32 * num_sms) return launch_shape<XT, RT, kNorm, 5, 8, 32>(p, s);
   // Block per row. A row alone on its SM is bound by latency, and more threads with a vector each
   // shorten it (1 x 5120: 1.95 against 2.3 us). Many rows want two vectors in flight per thread
-  // (2441 x 8192 bf16: 16.1 against 25.7 us), and past 8192 values four with half the threads, so
-  // that a row loads while another is stored (1220 x 16384 bf16: 15.5 against 18.4 us), but not
-  // where x and residual in fp32 would spill (46.5 against 54.2 us) or one wave takes all rows.
+  // (2441 x 8192 bf16: 16.1 against 25.7 us), and past 4096 values four with half the threads, so that
+  // a row loads while another is stored (2441 x 8192 bf16: 12.1 against 13.4 us, 1220 x 16384: 13.1
+  // against 18.4 us), but not where x and residual in fp32 would spill (46.5 against 54.2 us) or one
+  // wave takes all rows.
   if (p.n_rows <= num_sms && p.d <= 8192) return launch_shape<XT, RT, kNorm, 1, 8, 0>(p, s);
   constexpr bool kWide = kRes && sizeof(XT) == 4 && kResSize == 4;
   if constexpr (!kWide)
-    if (p.d > 8192 && p.n_rows > 4 * num_sms) return launch_shape<XT, RT, kNorm, 4, 8, 0>(p, s);
+    if (p.d > 4096 && p.n_rows > 4 * num_sms) return launch_shape<XT, RT, kNorm, 4, 8, 0>(p, s);
   return launch_shape<XT, RT, kNorm, 2, 8, 0>(p, s);
 }
 

@@ -66,6 +66,13 @@ struct Raw8<__nv_bfloat16, W> {
   __device__ __forceinline__ float2 pair(int i) const {
     return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   }
+  // m = max(m, |values|), NaN above all (as their bits order them, two at a time)
+  __device__ __forceinline__ void largest(float& m) const {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a = __vmaxu2(a, w[i] & 0x7FFF7FFFu);
+    m = max_abs_nan(m, __uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+  }
 };
 template <int W>
 struct Raw8<float, W> {
@@ -92,6 +99,10 @@ struct Raw8<float, W> {
     }
   }
   __device__ __forceinline__ float2 pair(int i) const { return v[i]; }
+  __device__ __forceinline__ void largest(float& m) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max_abs_nan(m, v[i].x, v[i].y);
+  }
 };
 
 template <int W>

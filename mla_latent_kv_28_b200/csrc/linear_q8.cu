@@ -8,8 +8,9 @@
 // M = 128 operand) times all tokens (N); its CTAs share the sum's length, each streaming its part of the
 // weights through a ring of TMA boxes into tcgen05 MMAs (kind::i8, int32 in tensor memory). Each CTA then
 // sends its partial sums to the CTAs that finish them (asynchronous stores into their shared memory,
-// counted by a barrier there: no second meeting), which add, scale and store. 33 x 16384 -> 5120 18.6 us
-// (4500 GB/s), 64 x 1536 -> 16384 9.0 us, 1 x 5120 -> 2112 5.4 to 6.0 us.
+// counted by a barrier there: no second meeting), which add, scale and store. 33 x 16384 -> 5120 18.1 us
+// (4700 GB/s), 64 x 1536 -> 16384 7.9 us, 1 x 5120 -> 2112 5.6 us (2 us of launch, 2 us until the boxes
+// are here and multiplied, 1 us of exchange).
 //
 // More tokens (linear_many): bound by the tensor core, and by the power that it takes. A pair of CTAs
 // (cta_group::2) takes 256 tokens x up to 256 channels: each CTA holds 128 of the tokens and half of the
@@ -109,8 +110,8 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// smem: ring of stages [128 x 128 weight box | n_tile x 128 token box], the partial sums that this CTA
-// receives, the barriers. Of the tile's 128 channels CTA r of the cluster finishes those from
+// smem: the barriers, the scales, a ring of stages [128 x 128 weight box | n_tile x 128 token box], the
+// partial sums that this CTA receives. Of the tile's 128 channels CTA r of the cluster finishes those from
 // ceil(128 r / splits) on: it gets from each CTA [its channels][4 tokens] pieces of 16 bytes, a
 // channel's pieces an odd number of 16-byte units from the next one's (no bank conflicts).
 template <typename OT>
@@ -124,7 +125,9 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
   const uint32_t full = sbase, empty = full + 8 * kMaxFewStages, done = empty + 8 * kMaxFewStages, received = done + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 16 * kMaxFewStages + 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 16 * kMaxFewStages + 20);
-  const uint32_t ring = sbase + 1024, parts = ring + p.ring;
+  float* a_scale = reinterpret_cast<float*>(smem + 1024);   // the tokens' scales, the tile's channels'
+  float* w_scale = a_scale + kFewRows;
+  const uint32_t ring = sbase + 2048, parts = ring + p.ring;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = p.splits, rank = splits > 1 ? (int)cluster_ctarank() : 0;
   const int f0 = (blockIdx.x / splits) * 128;
@@ -198,16 +201,21 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
       at.next(stages);
     }
     if (elect_one()) mma_commit(done);
+  } else if (warp >= 4) {
+    // the scales arrive while the tile is summed
+    const int i = tid - 128;
+    a_scale[i] = i < rows ? p.a_scale[i] : 0.f;
+    w_scale[i] = f0 + i < p.n ? p.w_scale[f0 + i] : 0.f;
   }
   __syncwarp();
   bool ok = wait_bounded(done, 0, guard);
-  __syncwarp();
+  __syncthreads();
   tc_fence_after();
 
   const int f = 32 * (warp & 3) + lane;   // this lane's channel of the tile
   const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
   if (splits == 1) {
-    const float w = f0 + f < p.n ? p.w_scale[f0 + f] : 0.f;
+    const float w = w_scale[f];
     for (int c0 = 16 * (warp >> 2); c0 < rows; c0 += 32) {
       uint32_t r[16];
       tmem_ld16_sync(lanes | (tmem + c0), r);
@@ -215,7 +223,7 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         if (c0 + j < rows && f0 + f < p.n)
-          store1(out + j * p.out_stride, (float)(int32_t)r[j] * w * p.a_scale[c0 + j]);
+          store1(out + j * p.out_stride, (float)(int32_t)r[j] * w * a_scale[c0 + j]);
     }
   } else {
     const int owner = f * splits >> 7, c = f - (128 * owner + splits - 1) / splits;
@@ -239,12 +247,12 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
           const int4 v = *reinterpret_cast<const int4*>(from + src * part);
           acc[0] += v.x; acc[1] += v.y; acc[2] += v.z; acc[3] += v.w;
         }
-        const float w = p.w_scale[col];
+        const float w = w_scale[c_begin + ch];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int t = 4 * q + j;
           if (t < rows)
-            store1(static_cast<OT*>(p.out) + (int64_t)t * p.out_stride + col, (float)acc[j] * w * p.a_scale[t]);
+            store1(static_cast<OT*>(p.out) + (int64_t)t * p.out_stride + col, (float)acc[j] * w * a_scale[t]);
         }
       }
     }
@@ -516,13 +524,13 @@ FewShape few_shape(const mla_decode_s& h, int tiles, int kblocks, int n_tile) {
       const uint32_t parts = splits == 1 ? 0 : splits * channels * (((uint32_t)n_tile / 4) | 1) * 16;
       const int per = (kblocks + splits - 1) / splits;
       const uint32_t limit = two ? kFewSmem : kFewSmemOne;
-      if (limit < parts + 2048 + stage) continue;
+      if (limit < parts + 3072 + stage) continue;
       FewShape f{};
       f.splits = splits;
-      f.stages = std::min({kMaxFewStages, (int)((limit - parts - 2048) / stage), per});
+      f.stages = std::min({kMaxFewStages, (int)((limit - parts - 3072) / stage), per});
       if (f.stages < std::min(3, per)) continue;
       f.ring = f.stages * stage;
-      f.smem = 2048 + f.ring + parts;
+      f.smem = 3072 + f.ring + parts;
       // In units of a k block's time: what an SM has to take, as often as not all clusters fit at once
       // (two CTAs on an SM slow each other down), and what a wave and the exchange cost beside it.
       const int clusters = h.few_clusters[f.smem <= kFewSmem][splits];

@@ -23,7 +23,7 @@
 
 #include "mla_internal.cuh"
 #include "rows.cuh"
-#include "sm100.cuh"
+#include "sm100_i8.cuh"
 
 namespace mla {
 namespace {

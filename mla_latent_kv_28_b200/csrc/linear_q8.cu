@@ -28,7 +28,7 @@
 
 #include "mla_internal.cuh"
 #include "rows.cuh"
-#include "sm100.cuh"
+#include "sm100_i8.cuh"
 
 namespace mla {
 namespace {
@@ -40,13 +40,6 @@ constexpr uint32_t kWBox = 128 * kBoxK;         // 128 rows of a box
 constexpr int kFewRows = 128;                   // tokens of linear_few: the MMA's N, in one piece
 constexpr int kMaxFewStages = 12;
 constexpr long long kWaitLimit = 2000000000LL;  // cycles: about a second
-
-// One lane of the warp, the same for all calls, so that what the loops below keep is uniform.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-  return e != 0;
-}
 
 // A ring position: the stage and how often the ring has been passed, mod 2.
 struct RingPos {
@@ -101,13 +94,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4], in
 __device__ __forceinline__ void load_scales(float (&w)[4], const float* scales, int col, int end, bool all) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) w[j] = (j == 0 || all) && col + j < end ? scales[col + j] : 0.f;
-}
-
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // smem: the barriers, the scales, a ring of stages [128 x 128 weight box | n_tile x 128 token box], the

@@ -20,7 +20,7 @@
 // instructions per value with packed fp32 pairs and two- and three-way maxima). Measured: 4096 x 5120
 // bf16 with an fp32 residual and y 42.4 us (6430 GB/s); 2048 x 16384 bf16 quantised 19.8 us (5090 GB/s),
 // the same in fp32 26.3 us (6390 GB/s); one row of 5120 2.1 us, the launch and one round trip. Rows of odd
-// width (one value at a time) take up to three times as long in bf16 (4882 x 4095 36 against 13 us).
+// width, one value at a time, take up to twice as long (4882 x 4095 against 4096, bf16: 22.7 and 13.0 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -295,6 +295,9 @@ cudaError_t launch_narrow(const NormParams& p, cudaStream_t s) {
   if (p.d <= 256) return launch_shape<XT, RT, kNorm, 1, W, 32>(p, s);
   if (p.d <= 512) return launch_shape<XT, RT, kNorm, 2, W, 32>(p, s);
   if (p.d <= 1024) return launch_shape<XT, RT, kNorm, 4, W, 32>(p, s);
+  // (4882 x 4095 bf16 quantised 22.7 against 27.7 us, in fp32 22.9 against 19.7; 2441 x 8191 36 against 31)
+  if constexpr (sizeof(XT) == 2)
+    if (p.d <= 4096) return launch_shape<XT, RT, kNorm, 1, W, 0>(p, s);
   return launch_shape<XT, RT, kNorm, 2, W, 0>(p, s);
 }
 

@@ -510,8 +510,8 @@ MLA_API int mla_decode_attn_noalloc(int32_t n_heads, float softmax_scale, int32_
  * Synchronise `stream`, then read and clear the handle's device error word. Returns MLA_OK
  * if it was clear, MLA_ERR_DEVICE_CHECK if a kernel set it (*detail, if not NULL, gets the
  * word: bit 0 = page-table entry out of range, bit 1 = a bounded wait ran out, bit 2 = a
- * kv_len outside 0..max_kv_len, clamped, or outside 1..max_kv_len in mla_append_kv), or
- * MLA_ERR_CUDA if the synchronisation itself failed.
+ * kv_len outside 0..max_kv_len, clamped, or outside 1..max_kv_len in mla_append_kv, or without room
+ * for its rows in mla_append_rows), or MLA_ERR_CUDA if the synchronisation itself failed.
  */
 MLA_API int mla_check_device_errors(mla_handle_t h, mla_stream_t stream, uint32_t* detail);
 

@@ -244,6 +244,26 @@ def test_bad_rows_set_error_bits_and_the_others_are_written():
     assert torch.equal(cache[t[2, 1], 36:38], good[t[2, 1], 36:38])
 
 
+def test_cache_past_32_bits():
+    """Rows behind 2^31 values of the pool, and positions of a long sequence."""
+    pages, length = 60_000, 3_000_000
+    cache = torch.zeros((pages, PAGE, 576), dtype=BF, device=DEV)
+    table = torch.arange(pages - length // PAGE - 1, pages, dtype=torch.int32, device=DEV)[None]
+    x, gamma = inputs(70, BF, 43)
+    lens, starts = torch.tensor([length], dtype=torch.int32, device=DEV), torch.tensor([0, 70], dtype=torch.int32, device=DEV)
+    with binding.MlaDecode(1, 1, length, page_size=PAGE) as h:
+        h.append_rows(x, gamma, cache, lens, starts, table)
+        h.check_device_errors()
+    pos = np.arange(length - 70, length)
+    theta = oracle.rope_theta(64, 10000.0)
+    ref, slack = expected_rows(x, gamma, pos, theta, 1e-6)
+    t = table[0].cpu().numpy()
+    got = cache[t[pos // PAGE].tolist(), (pos % PAGE).tolist()].double().cpu().numpy()
+    # the fp64 angle of a position p itself is off by p theta 2^-53: 3e6 * 2^-53 < 2^-31
+    assert np.all(np.abs(got - ref) <= np.abs(ref) * 2.0 ** -8 + 1.01 * slack + 2.0 ** -30)
+    assert int((cache != 0).any(dim=-1).sum()) == 70
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_graph_and_stream(fp8):
     new, cached = [5, 0, 70], [1, 2, 3]

@@ -108,6 +108,19 @@ def test_non_finite_and_zero_scales(handle, rows):
     assert torch.equal(out[3:][:, rest], clean[3:][:, rest]) and torch.equal(out[0, rest], clean[0, rest])
 
 
+@pytest.mark.parametrize("rows", [3, 130])
+def test_rows_far_apart(handle, rows):
+    """Offsets of rows past 2^31 in the codes and, in values, in the output."""
+    k, n = 200, 40
+    far = (2 ** 31 // (rows - 1) // 16 + 4) * 16
+    a = torch.zeros((rows - 1) * far + 256, dtype=torch.int8, device=DEV).as_strided((rows, k), (far, 1))
+    a.copy_(codes_of(rows, k, 60))
+    w, sa, sw = codes_of(n, k, 61), scales_of(rows, 62), scales_of(n, 63)
+    out = torch.zeros((rows - 1) * far + n, dtype=BF, device=DEV).as_strided((rows, n), (far, 1))
+    handle.linear_q8(a, sa, w, sw, out=out)
+    assert same(out, expected(a, sa, w, sw, BF))
+
+
 def test_no_rows(handle):
     w, sw = codes_of(8, 32, 21), scales_of(8, 22)
     assert handle.linear_q8(codes_of(0, 32, 23), torch.empty(0, device=DEV), w, sw).shape == (0, 8)

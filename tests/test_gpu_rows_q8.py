@@ -2,6 +2,8 @@
 (they depend on no rounding but the defined ones), scales and the normalised row to the rounding of
 their fp32 statistics."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -180,6 +182,41 @@ def test_codes_do_not_depend_on_layout_or_run(handle):
     other = handle.add_norm_q8(wide[:, 1:], g)
     again = handle.add_norm_q8(x, g)
     assert torch.equal(one[0], other[0]) and torch.equal(one[0], again[0]) and torch.equal(one[1], again[1])
+
+
+def test_rows_more_than_32_bits_apart(handle):
+    """Offsets of rows past 2^31 values, in the inputs and in the outputs."""
+    far, d = 1_100_000_008, 640
+    big = torch.zeros(2 * far + d, dtype=BF, device=DEV)
+    x = big.as_strided((3, d), (far, 1))
+    x.copy_(rows_of(3, d, BF, 25))
+    codes = torch.zeros(2 * far + d, dtype=torch.int8, device=DEV).as_strided((3, d), (far, 1))
+    want = handle.add_norm_q8(x.contiguous(), gamma_of(d), want_y=True)
+    got = handle.add_norm_q8(x, gamma_of(d), codes=codes, y=x)   # in place, far apart
+    assert torch.equal(want[0], codes) and torch.equal(want[1], got[1]) and torch.equal(want[3], x)
+
+
+def test_calls_from_two_threads(handle):
+    """The calls share nothing: two threads with a stream each, on one handle."""
+    data = [(rows_of(300, 1536, BF, 26 + i), gamma_of(1536, 28 + i)) for i in range(2)]
+    want = [handle.add_norm_q8(*a, want_y=True) for a in data]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(30):
+                got[i].append(handle.add_norm_q8(*data[i], want_y=True))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    for i in range(2):
+        assert len(got[i]) == 30
+        for out in got[i]:
+            assert all(torch.equal(want[i][j], out[j]) for j in (0, 1, 3))
 
 
 def test_other_stream_and_graph(handle):

@@ -517,12 +517,13 @@ FewShape few_shape(const mla_decode_s& h, int tiles, int kblocks, int n_tile) {
       if (f.stages < std::min(3, per)) continue;
       f.ring = f.stages * stage;
       f.smem = 3072 + f.ring + parts;
-      // In units of a k block's time: what an SM has to take, as often as not all clusters fit at once
-      // (two CTAs on an SM slow each other down), and what a wave and the exchange cost beside it.
-      const int clusters = h.few_clusters[f.smem <= kFewSmem][splits];
+      // In tenths of a k block's time: what a CTA has to take, as often as not all clusters fit at once
+      // (two CTAs on an SM slow each other down, the more tokens the more), and what a wave and the
+      // exchange cost beside it.
+      const int one = h.few_clusters[splits], clusters = one * (f.smem <= kFewSmem ? 2 : 1);
       if (clusters < 1) continue;
       const int64_t waves = (tiles + clusters - 1) / clusters;
-      const int64_t cost = waves * (10 * per * (tiles * splits > h.num_sms && f.smem <= kFewSmem ? 18 : 10) / 10 + 80) +
+      const int64_t cost = waves * (per * (std::min(tiles, clusters) > one ? 10 + n_tile / 8 : 10) + 80) +
                            (splits > 1 ? 20 : 0);
       if (cost < least) {
         least = cost;
@@ -615,23 +616,25 @@ cudaError_t init_linear_q8(mla_decode_s& h) {
     const cudaError_t e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
     if (e != cudaSuccess) return e;
   }
-  // a cluster stays within a group of SMs, so how many fit depends on the groups' sizes
-  for (const bool two : {false, true})
-    for (int splits = 1; splits <= kMaxSplits; ++splits) {
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = splits;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3(splits);
-      cfg.blockDim = dim3(256);
-      cfg.dynamicSmemBytes = two ? kFewSmem : kFewSmemOne;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      const cudaError_t e = cudaOccupancyMaxActiveClusters(&h.few_clusters[two][splits], linear_few<float>, &cfg);
-      if (e != cudaSuccess) return e;
-    }
+  // A cluster stays within a group of SMs, so how many fit depends on the groups' sizes. Asked for one
+  // CTA per SM: for two of a kernel that takes tensor memory the answer is still one, while two do run
+  // (1 x 5120 -> 2112 over 17 clusters of 8: 4.8 us, where 15 fit with one; 9 us over clusters of 7
+  // that leave room for one).
+  for (int splits = 1; splits <= kMaxSplits; ++splits) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(splits);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = kFewSmemOne;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&h.few_clusters[splits], linear_few<float>, &cfg);
+    if (e != cudaSuccess) return e;
+  }
   return cudaSuccess;
 }
 

@@ -73,7 +73,7 @@ struct mla_decode_s {
   int n_rows = 0;   // attention rows per sequence: n_heads * q_len (token-major)
   int group_rows = 0;   // rows per decode launch (the MMA's M = 128 at most); n_rows in groups
   double theta[mla::kDRope / 2] = {};  // RoPE pair frequencies (0: no rotation), YaRN applied
-  int few_clusters[2][mla::kMaxSplits + 1] = {};   // linear_q8: clusters that fit at once, [two CTAs per SM][CTAs]
+  int few_clusters[mla::kMaxSplits + 1] = {};   // linear_q8: clusters of so many CTAs that fit at once, one CTA per SM
   int units = 0;  // units the balanced plan cuts the tile space into
   mla::Workspace ws;
 };

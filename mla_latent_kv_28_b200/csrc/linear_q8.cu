@@ -8,8 +8,8 @@
 // M = 128 operand) times all tokens (N); its CTAs share the sum's length, each streaming its part of the
 // weights through a ring of TMA boxes into tcgen05 MMAs (kind::i8, int32 in tensor memory). Each CTA then
 // sends its partial sums to the CTAs that finish them (asynchronous stores into their shared memory,
-// counted by a barrier there: no second meeting), which add, scale and store. 33 x 16384 -> 5120 18.1 us
-// (4700 GB/s), 64 x 1536 -> 16384 7.9 us, 1 x 5120 -> 2112 5.6 us (2 us of launch, 2 us until the boxes
+// counted by a barrier there: no second meeting), which add, scale and store. 33 x 16384 -> 5120 17.7 us
+// (4700 GB/s), 64 x 1536 -> 16384 7.9 us, 1 x 5120 -> 2112 4.7 us (2 us of launch, 1.5 us until the boxes
 // are here and multiplied, 1 us of exchange).
 //
 // More tokens (linear_many): bound by the tensor core, and by the power that it takes. A pair of CTAs

@@ -336,15 +336,16 @@ cudaError_t launch_typed(const NormParams& p, int num_sms, cudaStream_t s) {
   if constexpr (!kRes)
     if (p.d <= 1280 && p.n_rows >= 32 * num_sms) return launch_shape<XT, RT, kNorm, 5, 8, 32>(p, s);
   // Block per row. A row alone on its SM is bound by latency, and more threads with a vector each
-  // shorten it (1 x 5120: 1.95 against 2.3 us). Many rows want two vectors in flight per thread
-  // (2441 x 8192 bf16: 16.1 against 25.7 us), and past 4096 values four with half the threads, so that
-  // a row loads while another is stored (2441 x 8192 bf16: 12.1 against 13.4 us, 1220 x 16384: 13.1
-  // against 18.4 us), but not where x and residual in fp32 would spill (46.5 against 54.2 us) or one
-  // wave takes all rows.
+  // shorten it (1 x 5120: 1.95 against 2.3 us). Many rows want two vectors in flight per thread (2441 x
+  // 8192 bf16 quantised 13.4 against 16.9 us), and where nothing is fp32 beside a residual four, with half
+  // the threads, so that rows load while others are stored: 4096 x 5120 bf16, normed, 16.4 against 19.4
+  // us, with a bf16 residual 23.7 against 25.6; with fp32 in it 43.9 against 42.2 (registers), and
+  // 2000 x 4096 quantised 7.5 against 6.9 (too few rows to fill the SMs with small blocks).
   if (p.n_rows <= num_sms && p.d <= 8192) return launch_shape<XT, RT, kNorm, 1, 8, 0>(p, s);
-  constexpr bool kWide = kRes && sizeof(XT) == 4 && kResSize == 4;
-  if constexpr (!kWide)
-    if (p.d > 4096 && p.n_rows > 4 * num_sms) return launch_shape<XT, RT, kNorm, 4, 8, 0>(p, s);
+  constexpr bool kFour = !kRes || (sizeof(XT) == 2 && kResSize == 2);
+  if constexpr (kFour)
+    if (p.d >= 2048 && p.n_rows * p.d >= (int64_t)num_sms * 81920)
+      return launch_shape<XT, RT, kNorm, 4, 8, 0>(p, s);
   return launch_shape<XT, RT, kNorm, 2, 8, 0>(p, s);
 }
 

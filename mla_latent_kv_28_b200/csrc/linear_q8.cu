@@ -70,30 +70,26 @@ struct FewParams {
   uint32_t* err;
 };
 
-// n of 4 neighbouring outputs (their rows are aligned for 4).
-__device__ __forceinline__ void store4(float* p, const float (&v)[4], int n) {
-  if (n >= 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    return;
-  }
+// 32 of a token's results into row `lane` of a box of 32 rows of 128 bytes (in bf16 half of the row, the
+// half-th), in the TMA's swizzle: 16-byte units, free of bank conflicts.
+__device__ __forceinline__ void put_row(uint32_t box, int lane, int, const float (&v)[32], const float*) {
 #pragma unroll
-  for (int j = 0; j < 3; ++j)
-    if (j < n) p[j] = v[j];
+  for (int u = 0; u < 8; ++u)
+    st_shared_v4(box + lane * 128 + ((u ^ (lane & 7)) << 4), __float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
+                 __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4], int n) {
-  if (n >= 4) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    return;
-  }
+__device__ __forceinline__ void put_row(uint32_t box, int lane, int half, const float (&v)[32], const __nv_bfloat16*) {
 #pragma unroll
-  for (int j = 0; j < 3; ++j)
-    if (j < n) p[j] = __float2bfloat16_rn(v[j]);
+  for (int u = 0; u < 4; ++u)
+    st_shared_v4(box + lane * 128 + (((u + 4 * half) ^ (lane & 7)) << 4), pack_bf16(v[8 * u], v[8 * u + 1]),
+                 pack_bf16(v[8 * u + 2], v[8 * u + 3]), pack_bf16(v[8 * u + 4], v[8 * u + 5]),
+                 pack_bf16(v[8 * u + 6], v[8 * u + 7]));
 }
-
-// The scales of columns col (and, if all, the three behind it) that lie before end.
-__device__ __forceinline__ void load_scales(float (&w)[4], const float* scales, int col, int end, bool all) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = (j == 0 || all) && col + j < end ? scales[col + j] : 0.f;
+// Value `col` of row `row` of such a box.
+template <typename OT>
+__device__ __forceinline__ OT get_one(const uint8_t* box, int row, int col) {
+  const int byte = col * (int)sizeof(OT);
+  return *reinterpret_cast<const OT*>(box + row * 128 + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15));
 }
 
 // smem: the barriers, the scales, a ring of stages [128 x 128 weight box | n_tile x 128 token box], the
@@ -254,11 +250,14 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
 // ------------------------------------------------------------------ many tokens
 
 constexpr int kMaxManyStages = 10;
-constexpr uint32_t kManyRing = 12 * kWBox;                  // 128 tokens + up to 128 channels a stage
 constexpr int kEpiWarps = 8;
-constexpr uint32_t kEpiBox = 32 * 128;                      // 32 rows x 128 bytes per warp
+constexpr int kEpiParts = kEpiWarps / 4, kPartCols = 256 / kEpiParts;   // the warps of a quarter share the columns
 constexpr int kManyThreads = 32 * (4 + kEpiWarps);
-constexpr uint32_t kManySmem = kManyRing + kEpiWarps * kEpiBox + 256 + 1024;
+// smem: a ring of boxes [128 tokens | half of the channels], the warps' channel scales, the barriers, and for
+// each warp a box of 32 rows of 128 bytes of results.
+constexpr uint32_t kManyRing = 11 * kWBox, kManyScales = kManyRing;
+constexpr uint32_t kManyBars = kManyScales + kEpiWarps * kPartCols * 4, kManyBoxes = kManyBars + 1024;
+constexpr uint32_t kManySmem = kManyBoxes + kEpiWarps * 4096 + 1024;
 
 struct ManyParams {
   int rows, n, n_tile, kblocks, tiles_m, tiles_n, group, stages;
@@ -267,7 +266,7 @@ struct ManyParams {
   const float* w_scale;
   void* out;
   int64_t out_stride;
-  bool vec;              // 4 neighbouring outputs can be stored at once
+  bool tma;              // the output's rows are aligned for TMA stores
   uint32_t* err;
 };
 
@@ -283,13 +282,14 @@ __device__ __forceinline__ void tile_at(const ManyParams& p, int t, int& tm, int
 template <typename OT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kManyThreads, 1)
 linear_many(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
-            const ManyParams p) {
+            const __grid_constant__ CUtensorMap tmap_out, const ManyParams p) {
+  constexpr int kCols = 128 / (int)sizeof(OT);   // columns of a box of results
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t epi = kManyRing, stage_bytes = kWBox + (uint32_t)p.n_tile / 2 * kBoxK;
+  const uint32_t stage_bytes = kWBox + (uint32_t)p.n_tile / 2 * kBoxK;
   const uint32_t stages = p.stages;
-  const uint32_t bars = sbase + epi + kEpiWarps * kEpiBox;
+  const uint32_t bars = sbase + kManyBars;
   const uint32_t full = bars, empty = bars + 8 * kMaxManyStages, acc_full = empty + 8 * kMaxManyStages,
                  acc_empty = acc_full + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (acc_empty + 16 - sbase));
@@ -313,6 +313,7 @@ linear_many(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
     *abort_flag = 0;
     prefetch_tmap(&tmap_w);
     prefetch_tmap(&tmap_a);
+    if (p.tma) prefetch_tmap(&tmap_out);
   }
   if (warp == 2) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
@@ -383,83 +384,105 @@ linear_many(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ 
       if (ok && elect_one()) mma_commit_pair(acc_full + 8 * as);
     }
   } else if (warp >= 4) {
-    // epilogue: warp w reads tensor memory lanes 32 (w % 4) .. + 32 (one token each) and half of the
-    // tile's columns, 32 at a time, and turns each 32 x 32 block round in shared memory (16-byte units,
-    // swizzled so that both directions are free of conflicts), so that a lane keeps its columns' scales
-    // and rows are written in whole sectors
-    const int quarter = warp & 3, per = p.n_tile / 2, first = ((warp - 4) >> 2) * per;
-    const uint32_t box = sbase + epi + (uint32_t)(warp - 4) * kEpiBox;
+    // Epilogue: warp w reads tensor memory lanes 32 (w % 4) .. + 32 (one token each) and every second of
+    // the tile's blocks of 128 bytes of columns. Its results go into a box and leave by TMA; where the
+    // output's rows are not aligned for that, or a tile ends inside a block, the warp stores them a row at
+    // a time. The scales of the next tile are on their way while this one is worked on, the channels' in
+    // shared memory, read by all lanes at once. (Rolled: a tile of a small product runs through here once,
+    // and instructions that are read once cost more than the rest.) 6244 x 320 -> 4704 in bf16 20.1 us:
+    // the chain of a block from tensor memory to its box, twice per SM sub-partition; with sixteen warps
+    // 18.6, but 120 against 115 us for 2048 x 16384 -> 5120, whose ring then has less room. Handing the
+    // accumulator back with a release at cluster scope, which waits for the stores, took 24.8.
+    const int quarter = warp & 3, part = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const uint32_t box = sbase + kManyBoxes + (uint32_t)(warp - 4) * 4096;
+    float* w_scale = reinterpret_cast<float*>(smem + kManyScales) + kPartCols * (warp - 4);
+    // (this warp's i-th 32 columns of a tile: its blocks are kEpiParts apart)
+    const auto column = [&](int i) {
+      return kCols * (part + kEpiParts * (32 * i / kCols)) + 32 * i % kCols;
+    };
+    float a_next = 0.f, w_next[kPartCols / 32];
+    const auto fetch = [&](int t) {
+      int tm, tn;
+      tile_at(p, t, tm, tn);
+      const int row = tm * 256 + (int)rank * 128 + 32 * quarter + lane;
+      a_next = row < p.rows ? p.a_scale[row] : 0.f;
+#pragma unroll
+      for (int i = 0; i < kPartCols / 32; ++i) {
+        const int c = column(i), col = tn * p.n_tile + c + lane;
+        w_next[i] = c < p.n_tile && col < p.n ? p.w_scale[col] : 0.f;
+      }
+    };
+    if (cluster < tiles) fetch(cluster);
     int it = 0;
     for (int t = cluster; t < tiles; t += clusters, ++it) {
       int tm, tn;
       tile_at(p, t, tm, tn);
       const int as = it & 1, row0 = tm * 256 + (int)rank * 128 + 32 * quarter;
-      // the scales arrive while the tile is summed: the token's, and those of this lane's column (or 4)
-      // of the first 32; the next 32 columns' follow while these are worked on
-      const float a_scale = row0 + lane < p.rows ? p.a_scale[row0 + lane] : 0.f;
-      const int begin = tn * p.n_tile + first, end = min(p.n, begin + per);
-      int col = begin + (p.vec ? 4 * (lane & 7) : lane);   // this lane's (first) column
-      float w[4];
-      load_scales(w, p.w_scale, col, end, p.vec);
+      const int begin = tn * p.n_tile;
+      const float a_scale = a_next;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kPartCols / 32; ++i) w_scale[32 * i + lane] = w_next[i];
+      __syncwarp();
+      if (t + clusters < tiles) fetch(t + clusters);
       const bool ok = wait_bounded(acc_full + 8 * as, (it >> 1) & 1, guard);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      // (rolled: a tile of a small product runs through here once, and instructions that are read once
-      // cost more than the rest)
 #pragma unroll 1
-      for (int c = 0; c < per; c += 32, col += 32) {
-        float w_next[4];
-        load_scales(w_next, p.w_scale, col + 32, end, p.vec);
-        {
-          uint32_t r[32];
-          tmem_ld32_sync(lanes | (tmem + 256 * as + first + c), r);
-          if (c + 32 >= per) {   // the accumulator is free
-            tc_fence_before();
-            if (lane == 0) mbar_arrive_remote(map_to_rank(acc_empty + 8 * as, 0));
-          }
-          __syncwarp();
+      for (int q = 0; q < kPartCols / 32; ++q) {
+        const int c = column(q), half = 32 * q % kCols / 32;
+        if (c >= p.n_tile) break;
+        uint32_t r[32];
+        tmem_ld32_sync(lanes | (tmem + 256 * as + c), r);
+        float v[32];
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            st_shared_v4(box + lane * 128 + ((u ^ (lane & 7)) << 4), r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+        for (int j = 0; j < 32; j += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(w_scale + 32 * q + j);
+          v[j] = (float)(int32_t)r[j] * w.x * a_scale;
+          v[j + 1] = (float)(int32_t)r[j + 1] * w.y * a_scale;
+          v[j + 2] = (float)(int32_t)r[j + 2] * w.z * a_scale;
+          v[j + 3] = (float)(int32_t)r[j + 3] * w.w * a_scale;
+        }
+        if (half == 0) {
+          if (lane == 0) bulk_wait_group_read<0>();   // the last store has read the box
           __syncwarp();
         }
-        const uint8_t* from = smem + (box - sbase);
-        if (p.vec) {
-          OT* out = static_cast<OT*>(p.out) + (int64_t)(row0 + (lane >> 3)) * p.out_stride + col;
-          int4 v[8];   // all reads before the first store: the compiler keeps their order
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + (lane >> 3);
-            v[i] = *reinterpret_cast<const int4*>(from + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + (lane >> 3);
-            const float a = __shfl_sync(0xffffffffu, a_scale, rr);
-            const float o[4] = {(float)v[i].x * w[0] * a, (float)v[i].y * w[1] * a, (float)v[i].z * w[2] * a,
-                                (float)v[i].w * w[3] * a};
-            if (row0 + rr < p.rows) store4(out + 4 * i * p.out_stride, o, end - col);
+        put_row(box, lane, half, v, static_cast<const OT*>(nullptr));
+        const int c0 = c - 32 * half, width = min(kCols, p.n_tile - c0);   // of the box
+        if (c + 32 < c0 + width) continue;   // its other half comes first
+        if (p.tma && width == kCols) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            // (what lies outside the output is not written)
+            if (begin + c0 < p.n && row0 < p.rows) tma_store_2d(&tmap_out, box, begin + c0, row0);
+            bulk_commit_group();
           }
         } else {
-          OT* out = static_cast<OT*>(p.out) + (int64_t)row0 * p.out_stride + col;
+          __syncwarp();
+          const int rows = min(32, p.rows - row0);
 #pragma unroll 1
-          for (int r0 = 0; r0 < 32; r0 += 8) {
-            int v[8];
+          for (int l = lane; l < width && begin + c0 + l < p.n; l += 32) {
+            OT* out = static_cast<OT*>(p.out) + (int64_t)row0 * p.out_stride + begin + c0 + l;
+#pragma unroll 1
+            for (int r0 = 0; r0 < rows; r0 += 8) {
+              OT o[8];   // (reads before stores: the compiler keeps their order)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              v[i] = *reinterpret_cast<const int*>(from + (r0 + i) * 128 + (((lane >> 2) ^ i) << 4) + 4 * (lane & 3));
+              for (int i = 0; i < 8; ++i) o[i] = get_one<OT>(smem + (box - sbase), r0 + i, l);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float a = __shfl_sync(0xffffffffu, a_scale, r0 + i);
-              if (row0 + r0 + i < p.rows && col < end) store1(out + (r0 + i) * p.out_stride, (float)v[i] * w[0] * a);
+              for (int i = 0; i < 8; ++i)
+                if (r0 + i < rows) out[(r0 + i) * p.out_stride] = o[i];
             }
           }
+          __syncwarp();
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = w_next[j];
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_relaxed(map_to_rank(acc_empty + 8 * as, 0));   // the accumulator is free
     }
+    if (lane == 0) bulk_wait_group0();   // the boxes are read before the block ends
   }
   __syncwarp();
   tc_fence_before();
@@ -491,6 +514,21 @@ bool encode(CUtensorMap* m, const int8_t* base, uint64_t rows, uint64_t k, uint6
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The output as a destination of boxes of 32 rows of 128 bytes.
+template <typename OT>
+bool encode_out(CUtensorMap* m, const LinearArgs& a) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.n, (cuuint64_t)a.rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.out_stride * sizeof(OT)};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / sizeof(OT)), 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, sizeof(OT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, a.out, dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr uint32_t kFewSmem = 113 * 1024, kFewSmemOne = 227 * 1024;   // two CTAs per SM, or one
@@ -568,8 +606,9 @@ int many_tile(const LinearArgs& a, int clusters) {
   for (int tile = 256; tile >= 32; tile -= 32) {
     const int64_t tiles = tiles_m * ((a.n + tile - 1) / tile), rounds = (tiles + clusters - 1) / clusters;
     // cycles, as measured: a k block of a tile (2 x tile of them are the MMAs' at tile 256; narrower tiles
-    // read as many tokens for less), and the last tile's 32-column blocks on their way out
-    const int64_t cost = rounds * kblocks * (220 + 14 * tile / 10) + (tile + 63) / 64 * 900;
+    // read as many tokens for less), and its results' way out, beside the next tile's sum but for the last
+    const int64_t sum = kblocks * (220 + 14 * tile / 10), store = 400 + (tile + 63) / 64 * 850;
+    const int64_t cost = rounds * std::max(sum, store) + std::min(sum, store);
     if (cost < least) {
       least = cost;
       best = tile;
@@ -588,20 +627,21 @@ cudaError_t launch_many(const mla_decode_s& h, const LinearArgs& a, cudaStream_t
   p.n_tile = many_tile(a, h.num_sms / 2);
   p.tiles_n = (a.n + p.n_tile - 1) / p.n_tile;
   p.group = 8;
-  p.stages = std::min<int>(kMaxManyStages, kManyRing / (kWBox + p.n_tile / 2 * kBoxK));
   p.idesc = idesc_i8_s32(256, p.n_tile);
   p.a_scale = a.scales;
   p.w_scale = a.w_scales;
   p.out = a.out;
   p.out_stride = a.out_stride;
-  p.vec = reinterpret_cast<uintptr_t>(a.out) % (4 * sizeof(OT)) == 0 && a.out_stride % 4 == 0;
+  p.tma = (reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.out_stride * sizeof(OT)) % 16 == 0;
+  p.stages = std::min<int>(kMaxManyStages, kManyRing / (kWBox + p.n_tile / 2 * kBoxK));
   p.err = h.ws.err;
-  CUtensorMap tw, ta;
+  CUtensorMap tw, ta, to{};
+  if (p.tma && !encode_out<OT>(&to, a)) return cudaErrorInvalidValue;
   if (!encode(&tw, a.w_codes, (uint64_t)a.n, (uint64_t)a.k, (uint64_t)a.w_stride, (uint32_t)p.n_tile / 2) ||
       !encode(&ta, a.codes, (uint64_t)a.rows, (uint64_t)a.k, (uint64_t)a.codes_stride, 128))
     return cudaErrorInvalidValue;
   const int clusters = std::min(h.num_sms / 2, p.tiles_m * p.tiles_n);
-  return launch_pdl(linear_many<OT>, dim3(2 * clusters), dim3(kManyThreads), kManySmem, s, tw, ta, p);
+  return launch_pdl(linear_many<OT>, dim3(2 * clusters), dim3(kManyThreads), kManySmem, s, tw, ta, to, p);
 }
 
 }  // namespace

@@ -16,6 +16,12 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   return d;
 }
 
+// Wait until all but the last N committed stores of this thread have read their source.
+template <int N>
+__device__ __forceinline__ void bulk_wait_group_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(N) : "memory");
+}
+
 // One lane of the warp, the same for all calls, so that what a whole warp's loop keeps is uniform.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;

@@ -4,20 +4,20 @@
 // so a result does not depend on how the sum is split; it is rounded when it becomes fp32, at each
 // of the two scales, and to the output's type.
 //
-// Up to 128 tokens (linear_few): bound by reading the weights. A cluster takes 128 output channels (the
-// M = 128 operand) times all tokens (N); its CTAs share the sum's length, each streaming its part of the
+// Few tokens (linear_few): bound by reading the weights. A cluster takes 128 output channels (the M = 128
+// operand) times up to 128 tokens (N); its CTAs share the sum's length, each streaming its part of the
 // weights through a ring of TMA boxes into tcgen05 MMAs (kind::i8, int32 in tensor memory). Each CTA then
 // sends its partial sums to the CTAs that finish them (asynchronous stores into their shared memory,
 // counted by a barrier there: no second meeting), which add, scale and store. 33 x 16384 -> 5120 17.7 us
-// (4700 GB/s), 64 x 1536 -> 16384 7.9 us, 1 x 5120 -> 2112 4.7 us (2 us of launch, 1.5 us until the boxes
+// (4700 GB/s), 64 x 1536 -> 16384 7.8 us, 1 x 5120 -> 2112 4.7 us (2 us of launch, 1.5 us until the boxes
 // are here and multiplied, 1 us of exchange).
 //
 // More tokens (linear_many): bound by the tensor core, and by the power that it takes. A pair of CTAs
 // (cta_group::2) takes 256 tokens x up to 256 channels: each CTA holds 128 of the tokens and half of the
 // channels, so a pair reads 64 KB per 128 steps of k for 256 x 256 results. Persistent, with the
 // accumulator double-buffered in tensor memory: eight warps scale and store a tile while the next is
-// summed. 2048 x 16384 -> 5120 116 us (2960 TOP/s; 136 us at the clocks of a long run), 8192 x 1536 ->
-// 8192 87 us (2370 TOP/s, its 128 MB of results beside it), 333 x 1000 -> 777 7 us.
+// summed. 2048 x 16384 -> 5120 115 us (2980 TOP/s; 135 us at the clocks of a long run), 8192 x 512 -> 8192
+// 40 us (its 134 MB of results), 333 x 1000 -> 777 6 to 8 us.
 //
 // In both the loops that issue copies and MMAs are run by whole warps with one elected lane, so that
 // descriptors and barriers stay in uniform registers: with a lone thread the 730 cycles of its own
@@ -96,7 +96,9 @@ __device__ __forceinline__ OT get_one(const uint8_t* box, int row, int col) {
 // partial sums that this CTA receives. Of the tile's 128 channels CTA r of the cluster finishes those from
 // ceil(128 r / splits) on: it gets from each CTA [its channels][4 tokens] pieces of 16 bytes, a
 // channel's pieces an odd number of 16-byte units from the next one's (no bank conflicts).
-template <typename OT>
+// kTiles: the tokens are cut into tiles too, one for each blockIdx.y (of its own, because the kernel of a few
+// microseconds was up to 0.7 us slower with the tile's offset in it: 128 x 1536 -> 16384).
+template <typename OT, bool kTiles>
 __global__ void __launch_bounds__(256)
 linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
            const FewParams p) {
@@ -112,10 +114,10 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
   const uint32_t ring = sbase + 2048, parts = ring + p.ring;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = p.splits, rank = splits > 1 ? (int)cluster_ctarank() : 0;
-  const int f0 = (blockIdx.x / splits) * 128;
+  const int f0 = (blockIdx.x / splits) * 128, t0 = kTiles ? blockIdx.y * p.n_tile : 0;
   const int kb0 = (int)((int64_t)p.kblocks * rank / splits), kb1 = (int)((int64_t)p.kblocks * (rank + 1) / splits);
   const uint32_t tmem_cols = p.n_tile <= 32 ? 32u : p.n_tile <= 64 ? 64u : 128u;
-  const int rows = p.rows, quads = (rows + 3) / 4;
+  const int rows = kTiles ? min(p.n_tile, p.rows - t0) : p.rows, quads = (rows + 3) / 4;
   const int c_begin = (128 * rank + splits - 1) / splits, c_count = (128 * (rank + 1) + splits - 1) / splits - c_begin;
   const uint32_t pitch = (uint32_t)(quads | 1) * 16;          // bytes between a part's channels
   const uint32_t part = (uint32_t)((128 + splits - 1) / splits) * pitch;   // ... between the parts
@@ -157,7 +159,7 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
         const uint32_t bar = full + 8 * at.stage, dst = ring + at.stage * stage_bytes;
         mbar_arrive_expect_tx(bar, stage_bytes);
         tma_load_2d(dst, &tmap_w, kb * kBoxK, f0, bar);
-        tma_load_2d(dst + kWBox, &tmap_a, kb * kBoxK, 0, bar);
+        tma_load_2d(dst + kWBox, &tmap_a, kb * kBoxK, t0, bar);
       }
       at.next(stages);
     }
@@ -186,7 +188,7 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
   } else if (warp >= 4) {
     // the scales arrive while the tile is summed
     const int i = tid - 128;
-    a_scale[i] = i < rows ? p.a_scale[i] : 0.f;
+    a_scale[i] = i < rows ? p.a_scale[t0 + i] : 0.f;
     w_scale[i] = f0 + i < p.n ? p.w_scale[f0 + i] : 0.f;
   }
   __syncwarp();
@@ -201,7 +203,7 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
     for (int c0 = 16 * (warp >> 2); c0 < rows; c0 += 32) {
       uint32_t r[16];
       tmem_ld16_sync(lanes | (tmem + c0), r);
-      OT* out = static_cast<OT*>(p.out) + (int64_t)c0 * p.out_stride + f0 + f;
+      OT* out = static_cast<OT*>(p.out) + (int64_t)(t0 + c0) * p.out_stride + f0 + f;
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         if (c0 + j < rows && f0 + f < p.n)
@@ -234,7 +236,7 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
         for (int j = 0; j < 4; ++j) {
           const int t = 4 * q + j;
           if (t < rows)
-            store1(static_cast<OT*>(p.out) + (int64_t)t * p.out_stride + col, (float)acc[j] * w * a_scale[t]);
+            store1(static_cast<OT*>(p.out) + (int64_t)(t0 + t) * p.out_stride + col, (float)acc[j] * w * a_scale[t]);
         }
       }
     }
@@ -533,15 +535,19 @@ bool encode_out(CUtensorMap* m, const LinearArgs& a) {
 
 constexpr uint32_t kFewSmem = 113 * 1024, kFewSmemOne = 227 * 1024;   // two CTAs per SM, or one
 
-// How linear_few cuts its work: the CTAs that share a tile's sum, and the stages of their rings.
+// How linear_few cuts its work: the tokens of a tile, the CTAs that share its sum, the stages of their
+// rings, and about how long it takes.
 struct FewShape {
-  int splits, stages;
+  int n_tile, row_tiles, splits, stages;
   uint32_t ring, smem;
+  int64_t ns = INT64_MAX, capped_ns = INT64_MAX;
 };
-FewShape few_shape(const mla_decode_s& h, int tiles, int kblocks, int n_tile) {
+FewShape few_shape(const mla_decode_s& h, const LinearArgs& a) {
+  const int row_tiles = (a.rows + kFewRows - 1) / kFewRows, kblocks = (a.k + kBoxK - 1) / kBoxK;
+  const int n_tile = ((a.rows + row_tiles - 1) / row_tiles + 15) / 16 * 16;
+  const int64_t tiles = (int64_t)((a.n + 127) / 128) * row_tiles;
   const uint32_t stage = kWBox + (uint32_t)n_tile * kBoxK;
   FewShape best{};
-  int64_t least = INT64_MAX;
   for (int splits = 1; splits <= kMaxSplits && (splits == 1 || kblocks >= 2 * splits); ++splits)
     for (const bool two : {false, true}) {
       const uint32_t channels = (128 + splits - 1) / splits;   // of a CTA, at most
@@ -549,38 +555,35 @@ FewShape few_shape(const mla_decode_s& h, int tiles, int kblocks, int n_tile) {
       const int per = (kblocks + splits - 1) / splits;
       const uint32_t limit = two ? kFewSmem : kFewSmemOne;
       if (limit < parts + 3072 + stage) continue;
-      FewShape f{};
-      f.splits = splits;
+      FewShape f{n_tile, row_tiles, splits};
       f.stages = std::min({kMaxFewStages, (int)((limit - parts - 3072) / stage), per});
       if (f.stages < std::min(3, per)) continue;
       f.ring = f.stages * stage;
       f.smem = 3072 + f.ring + parts;
-      // In tenths of a k block's time: what a CTA has to take, as often as not all clusters fit at once
-      // (two CTAs on an SM slow each other down, the more tokens the more), and what a wave and the
-      // exchange cost beside it.
+      // A k block arrives at some 110 bytes a nanosecond (two CTAs on an SM slow each other down, the more
+      // tokens the more), as often as not all clusters fit at once; set-up, and the exchange of the
+      // partial sums at 16 bytes a store.
       const int one = h.few_clusters[splits], clusters = one * (f.smem <= kFewSmem ? 2 : 1);
       if (clusters < 1) continue;
-      const int64_t waves = (tiles + clusters - 1) / clusters;
-      const int64_t cost = waves * (per * (std::min(tiles, clusters) > one ? 10 + n_tile / 8 : 10) + 80) +
-                           (splits > 1 ? 20 : 0);
-      if (cost < least) {
-        least = cost;
-        best = f;
-      }
+      const int64_t waves = (tiles + clusters - 1) / clusters, at_once = std::min<int64_t>(tiles, clusters);
+      const int64_t arrival = waves * per * (int64_t)(stage / 110) * (at_once > one ? 10 + n_tile / 8 : 10) / 10;
+      const int64_t rest = 1600 + waves * 1400 + (splits > 1 ? 340 + 30 * n_tile : 10 * n_tile);
+      if (arrival + rest >= best.ns) continue;
+      best = f;
+      best.ns = arrival + rest;
+      // (against linear_many, not between the splits: all CTAs together get some 9600 bytes a nanosecond)
+      best.capped_ns = std::max<int64_t>(arrival, waves * per * (int64_t)stage * at_once * splits / 9600) + rest;
     }
   return best;
 }
 
 template <typename OT>
-cudaError_t launch_few(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s) {
+cudaError_t launch_few(const mla_decode_s& h, const LinearArgs& a, const FewShape& f, cudaStream_t s) {
   FewParams p{};
   p.rows = a.rows;
   p.n = a.n;
-  p.n_tile = (a.rows + 15) / 16 * 16;
+  p.n_tile = f.n_tile;
   p.kblocks = (a.k + kBoxK - 1) / kBoxK;
-  const int blocks = (a.n + 127) / 128;
-  const FewShape f = few_shape(h, blocks, p.kblocks, p.n_tile);
-  if (f.splits == 0) return cudaErrorInvalidValue;
   p.splits = f.splits;
   p.stages = f.stages;
   p.ring = f.ring;
@@ -594,37 +597,39 @@ cudaError_t launch_few(const mla_decode_s& h, const LinearArgs& a, cudaStream_t 
   p.out = a.out;
   p.out_stride = a.out_stride;
   p.err = h.ws.err;
-  return launch_pdl_cluster(linear_few<OT>, dim3(blocks * p.splits), dim3(256), f.smem, p.splits, s, tw, ta, p);
+  const auto kernel = f.row_tiles > 1 ? linear_few<OT, true> : linear_few<OT, false>;
+  return launch_pdl_cluster(kernel, dim3((a.n + 127) / 128 * p.splits, f.row_tiles), dim3(256), f.smem, p.splits, s, tw,
+                            ta, p);
 }
 
-// The channels per tile: the pairs work in rounds, a tile each, so what a round takes counts as often
-// as there are rounds.
-int many_tile(const LinearArgs& a, int clusters) {
-  const int64_t kblocks = (a.k + kBoxK - 1) / kBoxK, tiles_m = (a.rows + 255) / 256;
-  int best = 256;
-  int64_t least = INT64_MAX;
+// linear_many's channels per tile, and about how long it takes: the pairs work in rounds, a tile each, so
+// what a round takes counts as often as there are rounds.
+struct ManyShape {
+  int n_tile = 0;
+  int64_t ns = INT64_MAX;
+};
+ManyShape many_shape(const mla_decode_s& h, const LinearArgs& a) {
+  const int64_t kblocks = (a.k + kBoxK - 1) / kBoxK, tiles_m = (a.rows + 255) / 256, clusters = h.num_sms / 2;
+  ManyShape best;
   for (int tile = 256; tile >= 32; tile -= 32) {
     const int64_t tiles = tiles_m * ((a.n + tile - 1) / tile), rounds = (tiles + clusters - 1) / clusters;
     // cycles, as measured: a k block of a tile (2 x tile of them are the MMAs' at tile 256; narrower tiles
     // read as many tokens for less), and its results' way out, beside the next tile's sum but for the last
     const int64_t sum = kblocks * (220 + 14 * tile / 10), store = 400 + (tile + 63) / 64 * 850;
-    const int64_t cost = rounds * std::max(sum, store) + std::min(sum, store);
-    if (cost < least) {
-      least = cost;
-      best = tile;
-    }
+    const int64_t ns = 4000 + (rounds * std::max(sum, store) + std::min(sum, store)) * 4 / 7;
+    if (ns < best.ns) best = ManyShape{tile, ns};
   }
   return best;
 }
 
 template <typename OT>
-cudaError_t launch_many(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s) {
+cudaError_t launch_many(const mla_decode_s& h, const LinearArgs& a, int n_tile, cudaStream_t s) {
   ManyParams p{};
   p.rows = a.rows;
   p.n = a.n;
   p.kblocks = (a.k + kBoxK - 1) / kBoxK;
   p.tiles_m = (a.rows + 255) / 256;
-  p.n_tile = many_tile(a, h.num_sms / 2);
+  p.n_tile = n_tile;
   p.tiles_n = (a.n + p.n_tile - 1) / p.n_tile;
   p.group = 8;
   p.idesc = idesc_i8_s32(256, p.n_tile);
@@ -648,8 +653,10 @@ cudaError_t launch_many(const mla_decode_s& h, const LinearArgs& a, cudaStream_t
 
 cudaError_t init_linear_q8(mla_decode_s& h) {
   const struct { const void* kernel; uint32_t smem; } need[] = {
-      {reinterpret_cast<const void*>(linear_few<float>), kFewSmemOne},
-      {reinterpret_cast<const void*>(linear_few<__nv_bfloat16>), kFewSmemOne},
+      {reinterpret_cast<const void*>(linear_few<float, false>), kFewSmemOne},
+      {reinterpret_cast<const void*>(linear_few<float, true>), kFewSmemOne},
+      {reinterpret_cast<const void*>(linear_few<__nv_bfloat16, false>), kFewSmemOne},
+      {reinterpret_cast<const void*>(linear_few<__nv_bfloat16, true>), kFewSmemOne},
       {reinterpret_cast<const void*>(linear_many<float>), kManySmem},
       {reinterpret_cast<const void*>(linear_many<__nv_bfloat16>), kManySmem}};
   for (const auto& k : need) {
@@ -672,15 +679,22 @@ cudaError_t init_linear_q8(mla_decode_s& h) {
     cfg.dynamicSmemBytes = kFewSmemOne;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&h.few_clusters[splits], linear_few<float>, &cfg);
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&h.few_clusters[splits], linear_few<float, false>, &cfg);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
 cudaError_t launch_linear_q8(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s) {
-  if (a.rows <= kFewRows) return a.out_f32 ? launch_few<float>(h, a, s) : launch_few<__nv_bfloat16>(h, a, s);
-  return a.out_f32 ? launch_many<float>(h, a, s) : launch_many<__nv_bfloat16>(h, a, s);
+  // Up to 64 tokens always linear_few (a pair's tile of 256 is mostly empty); of more, the one that should
+  // be done first: few channels under a long sum are one pair's work for long, while clusters share it
+  // (491 x 14864 -> 172 12.2 against 27.3 us, 128 x 1536 -> 16384 8.8 against 10.1; 512 x 5120 -> 2112 17
+  // against 12.2, 100 x 2048 -> 2048 8.0 against 6.8).
+  const FewShape f = few_shape(h, a);
+  const ManyShape m = a.rows <= 64 ? ManyShape{} : many_shape(h, a);
+  if (f.capped_ns < m.ns) return a.out_f32 ? launch_few<float>(h, a, f, s) : launch_few<__nv_bfloat16>(h, a, f, s);
+  if (m.n_tile == 0) return cudaErrorInvalidValue;
+  return a.out_f32 ? launch_many<float>(h, a, m.n_tile, s) : launch_many<__nv_bfloat16>(h, a, m.n_tile, s);
 }
 
 }  // namespace mla

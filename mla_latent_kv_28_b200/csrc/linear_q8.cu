@@ -533,6 +533,7 @@ bool encode_out(CUtensorMap* m, const LinearArgs& a) {
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr uint32_t kFewHead = 3 * 1024;   // barriers and scales, 1024 bytes each, and what aligns them
 constexpr uint32_t kFewSmem = 113 * 1024, kFewSmemOne = 227 * 1024;   // two CTAs per SM, or one
 
 // How linear_few cuts its work: the tokens of a tile, the CTAs that share its sum, the stages of their
@@ -548,18 +549,20 @@ FewShape few_shape(const mla_decode_s& h, const LinearArgs& a) {
   const int64_t tiles = (int64_t)((a.n + 127) / 128) * row_tiles;
   const uint32_t stage = kWBox + (uint32_t)n_tile * kBoxK;
   FewShape best{};
-  for (int splits = 1; splits <= kMaxSplits && (splits == 1 || kblocks >= 2 * splits); ++splits)
+  // (tokens in several tiles only where the sum is shared: of a short sum linear_many's tiles read less and
+  // their results leave while the next is summed: 2821 x 192 -> 1520 6.2 against 9.4 us)
+  for (int splits = row_tiles > 1 ? 2 : 1; splits <= kMaxSplits && (splits == 1 || kblocks >= 2 * splits); ++splits)
     for (const bool two : {false, true}) {
       const uint32_t channels = (128 + splits - 1) / splits;   // of a CTA, at most
       const uint32_t parts = splits == 1 ? 0 : splits * channels * (((uint32_t)n_tile / 4) | 1) * 16;
       const int per = (kblocks + splits - 1) / splits;
       const uint32_t limit = two ? kFewSmem : kFewSmemOne;
-      if (limit < parts + 3072 + stage) continue;
+      if (limit < parts + kFewHead + stage) continue;
       FewShape f{n_tile, row_tiles, splits};
-      f.stages = std::min({kMaxFewStages, (int)((limit - parts - 3072) / stage), per});
+      f.stages = std::min({kMaxFewStages, (int)((limit - parts - kFewHead) / stage), per});
       if (f.stages < std::min(3, per)) continue;
       f.ring = f.stages * stage;
-      f.smem = 3072 + f.ring + parts;
+      f.smem = kFewHead + f.ring + parts;
       // A k block arrives at some 110 bytes a nanosecond (two CTAs on an SM slow each other down, the more
       // tokens the more), as often as not all clusters fit at once; set-up, and the exchange of the
       // partial sums at 16 bytes a store.
@@ -567,7 +570,7 @@ FewShape few_shape(const mla_decode_s& h, const LinearArgs& a) {
       if (clusters < 1) continue;
       const int64_t waves = (tiles + clusters - 1) / clusters, at_once = std::min<int64_t>(tiles, clusters);
       const int64_t arrival = waves * per * (int64_t)(stage / 110) * (at_once > one ? 10 + n_tile / 8 : 10) / 10;
-      const int64_t rest = 1600 + waves * 1400 + (splits > 1 ? 340 + 30 * n_tile : 10 * n_tile);
+      const int64_t rest = (row_tiles > 1 ? 2100 : 1600) + waves * 1400 + (splits > 1 ? 340 + 30 * n_tile : 10 * n_tile);
       if (arrival + rest >= best.ns) continue;
       best = f;
       best.ns = arrival + rest;
@@ -688,8 +691,8 @@ cudaError_t init_linear_q8(mla_decode_s& h) {
 cudaError_t launch_linear_q8(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s) {
   // Up to 64 tokens always linear_few (a pair's tile of 256 is mostly empty); of more, the one that should
   // be done first: few channels under a long sum are one pair's work for long, while clusters share it
-  // (491 x 14864 -> 172 12.2 against 27.3 us, 128 x 1536 -> 16384 8.8 against 10.1; 512 x 5120 -> 2112 17
-  // against 12.2, 100 x 2048 -> 2048 8.0 against 6.8).
+  // (us, linear_few against linear_many: 491 x 14864 -> 172 12.2 and 27.3, 128 x 1536 -> 16384 8.8 and 10.1,
+  // 195 x 15913 -> 2655 29 and 44; 512 x 5120 -> 2112 17 and 12.2, 2821 x 192 -> 1520 9.4 and 6.2).
   const FewShape f = few_shape(h, a);
   const ManyShape m = a.rows <= 64 ? ManyShape{} : many_shape(h, a);
   if (f.capped_ns < m.ns) return a.out_f32 ? launch_few<float>(h, a, f, s) : launch_few<__nv_bfloat16>(h, a, f, s);

@@ -460,6 +460,13 @@ class MlaDecode:
         """The stream to launch on: the current one of the handle's device unless given."""
         return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else stream.cuda_stream
 
+    def _outputs_on(self, stream):
+        """For a call on a stream that need not be the current one: tensors that the call makes belong to
+        the stream that writes them (memory freed on the current one may still be in use there)."""
+        if stream.device.index != self.device:
+            raise ValueError(f"stream: expected one of cuda:{self.device}, got one of {stream.device}")
+        return torch.cuda.stream(stream)
+
     def _rows(self, t: torch.Tensor, name: str, dtypes, shape=None) -> int:
         """The stride between the rows of a [rows, d] tensor on the handle's device."""
         sizes, strides = t.shape, t.stride()
@@ -502,6 +509,9 @@ class MlaDecode:
         bf16. Returns (codes int8 [rows, d], scales fp32 [rows], residual_out, y): residual_out is
         r in the residual's type (a new tensor unless given; `residual` itself is allowed), None
         without a residual; y is the normalised row in bf16, None unless wanted or given."""
+        if stream is not None:
+            with self._outputs_on(stream):
+                return self.add_norm_q8(x, gamma, residual, eps, want_y, residual_out, codes, scales, y)
         x_stride = self._rows(x, "x", ROW_TYPES)
         rows, d = shape = x.shape
         device = x.device
@@ -528,20 +538,23 @@ class MlaDecode:
                 res_stride, 0 if residual is None else residual_out.data_ptr(), out_stride, gamma.data_ptr(),
                 0 if y is None else y.data_ptr(), y_stride, codes.data_ptr(), codes_stride, scales.data_ptr(),
                 res_type, eps)
-            _check(self._lib.mla_add_norm_q8(self._h, args, self._here(stream)), "mla_add_norm_q8")
+            _check(self._lib.mla_add_norm_q8(self._h, args, self._here(None)), "mla_add_norm_q8")
         return codes, scales, residual_out, y
 
     def quantize_rows(self, x: torch.Tensor, codes: Optional[torch.Tensor] = None,
                       scales: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """int8 codes of the rows of x [rows, d] (bf16 or fp32) and a scale for each: the input of
         linear_q8, or its weight (x [n, k], a scale per output channel)."""
+        if stream is not None:
+            with self._outputs_on(stream):
+                return self.quantize_rows(x, codes, scales)
         x_stride = self._rows(x, "x", ROW_TYPES)
         rows, d = x.shape
         codes, codes_stride, scales = self._new_codes(rows, d, codes, scales, x.device)
         if rows > 0:
             args = QUANTIZE_ARGS.pack(rows, d, ROW_TYPES[x.dtype], x.data_ptr(), x_stride, codes.data_ptr(),
                                       codes_stride, scales.data_ptr())
-            _check(self._lib.mla_quantize_rows(self._h, args, self._here(stream)), "mla_quantize_rows")
+            _check(self._lib.mla_quantize_rows(self._h, args, self._here(None)), "mla_quantize_rows")
         return codes, scales
 
     def linear_q8(self, codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
@@ -549,6 +562,9 @@ class MlaDecode:
         """out[i, j] = (codes[i] . w_codes[j]) * w_scales[j] * scales[i]: codes [rows, k] and
         w_codes [n, k] int8, rows 16-byte aligned; scales [rows], w_scales [n] fp32. out [rows, n]
         bf16 or fp32 (out_dtype unless given)."""
+        if stream is not None:
+            with self._outputs_on(stream):
+                return self.linear_q8(codes, scales, w_codes, w_scales, out, out_dtype)
         a_stride = self._rows(codes, "codes", _INT8)
         rows, k = codes.shape
         w_stride = self._rows(w_codes, "w_codes", _INT8)
@@ -572,7 +588,7 @@ class MlaDecode:
         if rows > 0:
             args = LINEAR_ARGS.pack(rows, k, n, ROW_TYPES[out_dtype], codes.data_ptr(), a_stride, scales.data_ptr(),
                                     w_codes.data_ptr(), w_stride, w_scales.data_ptr(), out.data_ptr(), out_stride)
-            _check(self._lib.mla_linear_q8(self._h, args, self._here(stream)), "mla_linear_q8")
+            _check(self._lib.mla_linear_q8(self._h, args, self._here(None)), "mla_linear_q8")
         return out
 
     def _append_rows(self, call, x, gamma, cache, cache_type, exps, kv_lens, row_starts, page_table, eps, stream):

@@ -164,3 +164,14 @@ def test_tensors_of_another_device_are_refused(handle):
         lambda: handle.add_norm_q8(x, torch.zeros(576, dtype=BF)), lambda: handle.quantize_rows(x),
         lambda: handle.linear_q8(a, s, a, s), lambda: handle.append_rows(x, g, torch.zeros((2, 100, 576), dtype=BF), lens),
     ])
+
+
+def test_streams_of_another_device_are_refused(handle):
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 3), 5
+    a, s = torch.zeros((2, 16), dtype=torch.int8), torch.zeros(2)
+    refused(handle, [
+        lambda: handle.add_norm_q8(torch.zeros((2, 16)), torch.zeros(16, dtype=BF), stream=Stream()),
+        lambda: handle.quantize_rows(torch.zeros((2, 16)), stream=Stream()),
+        lambda: handle.linear_q8(a, s, a, s, stream=Stream()),
+    ])

@@ -238,6 +238,28 @@ def test_other_stream_and_graph(handle):
     assert torch.equal(q[0], handle.quantize_rows(want[3])[0])
 
 
+@pytest.mark.parametrize("call", ["norm", "quantize", "linear"])
+def test_new_outputs_belong_to_the_stream_that_writes_them(handle, call):
+    """Memory that the current stream has freed but still writes is not the other stream's output."""
+    rows, d = 256, 1024
+    x, g = rows_of(rows, d, BF, 31), gamma_of(d)
+    codes, scales = handle.quantize_rows(x)
+    run = {"norm": lambda s: handle.add_norm_q8(x, g, want_y=True, stream=s)[3],
+           "quantize": lambda s: handle.quantize_rows(x, stream=s)[0],
+           "linear": lambda s: handle.linear_q8(codes, scales, codes, scales, out_dtype=F32, stream=s)}[call]
+    want = run(None).clone()
+    big, s = torch.empty(1 << 28, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    taken = torch.empty_like(want)
+    for _ in range(20):
+        big.fill_(1.0)
+    taken.fill_(5)
+    del taken
+    got = run(s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_refusals(handle):
     x, g = rows_of(4, 64, BF, 19), gamma_of(64)
     for call in (lambda: handle.add_norm_q8(x.cpu(), g), lambda: handle.add_norm_q8(x.half(), g),

@@ -327,9 +327,10 @@ MLA_API int mla_append_kv_fp8(mla_handle_t h, int32_t batch, int32_t d_model, co
  *   columns (no residual) -> mla_linear_q8 with W^UQ and with W^QR; mla_append_rows on the other
  *   576 columns; mla_decode_step; mla_quantize_rows -> mla_linear_q8 with W^O.
  * These calls take their arguments as a struct (read before the call returns) and use the handle's
- * device whichever device is current, and no workspace: several may run at once. Rows may lie apart (a stride in elements between rows, at least the row's
- * length); where a call says nothing else a pointer needs its elements' alignment only. n_rows 0
- * is valid and does nothing. Outputs must not overlap inputs, but for those named.
+ * device whichever device is current, and no workspace: several may run at once. Rows may lie apart
+ * (a stride in elements between rows, at least the row's length); where a call says nothing else a
+ * pointer needs its elements' alignment only. n_rows 0 is valid and does nothing. Outputs must not
+ * overlap inputs, but for those named.
  */
 enum {
   MLA_BF16 = 0,

@@ -55,6 +55,19 @@ def test_shapes(handle, rows, k, n, dtype):
     assert same(out, expected(a, sa, w, sw, dtype))
 
 
+@pytest.mark.parametrize("rows,k,n", [(129, 5120, 33), (191, 9921, 65), (200, 16384, 130), (300, 9920, 64),
+                                      (486, 10284, 417), (1025, 8192, 48), (2319, 11392, 17)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_sums_of_several_tiles_of_tokens(handle, rows, k, n, dtype):
+    a, w, sa, sw = codes_of(rows, k, 31), codes_of(n, k, 32), scales_of(rows, 33), scales_of(n, 34)
+    block = torch.full((rows + 2, n + 3), 7.0, dtype=dtype, device=DEV)
+    handle.linear_q8(a, sa, w, sw, out=block[1:rows + 1, 1:n + 1])
+    handle.check_device_errors()
+    assert same(block[1:rows + 1, 1:n + 1], expected(a, sa, w, sw, dtype))
+    block[1:rows + 1, 1:n + 1] = 7.0
+    assert bool((block == 7.0).all())
+
+
 @pytest.mark.parametrize("rows", [1, 7, 128, 129, 300])
 def test_largest_sums(handle, rows):
     """The longest sum of the largest products, and of the largest negative ones."""

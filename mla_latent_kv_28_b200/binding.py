@@ -467,17 +467,18 @@ class MlaDecode:
             raise ValueError(f"stream: expected one of cuda:{self.device}, got one of {stream.device}")
         return torch.cuda.stream(stream)
 
-    def _rows(self, t: torch.Tensor, name: str, dtypes, shape=None) -> int:
-        """The stride between the rows of a [rows, d] tensor on the handle's device."""
-        sizes, strides = t.shape, t.stride()
-        if len(strides) == 2 and t.dtype in dtypes and t.get_device() == self.device and \
+    def _rows(self, t: torch.Tensor, name: str, dtypes, shape=None) -> Tuple[int, int, int]:
+        """Rows, width and the stride between the rows of a [rows, d] tensor on the handle's device."""
+        sizes = t.shape
+        if len(sizes) == 2 and t.dtype in dtypes and t.get_device() == self.device and \
                 (shape is None or sizes == shape):
             rows, d = sizes
-            if strides[1] == 1 or d <= 1:
+            stride, inner = t.stride()
+            if inner == 1 or d <= 1:
                 if rows <= 1:
-                    return d
-                if strides[0] >= d:
-                    return strides[0]
+                    return rows, d, d
+                if stride >= d:
+                    return rows, d, stride
         raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dtypes)} "
                          f"{'[rows, d]' if shape is None else tuple(shape)} with unit inner stride and rows "
                          f"apart on cuda:{self.device}, got {_shape(t)}")
@@ -493,7 +494,7 @@ class MlaDecode:
             stride = (d + 15) // 16 * 16
             codes = torch.empty_strided((rows, d), (stride, 1), dtype=torch.int8, device=device)
         else:
-            stride = self._rows(codes, "codes", _INT8, (rows, d))
+            _, _, stride = self._rows(codes, "codes", _INT8, (rows, d))
         if scales is None:
             scales = torch.empty_strided((rows,), (1,), dtype=torch.float32, device=device)
         else:
@@ -512,24 +513,23 @@ class MlaDecode:
         if stream is not None:
             with self._outputs_on(stream):
                 return self.add_norm_q8(x, gamma, residual, eps, want_y, residual_out, codes, scales, y)
-        x_stride = self._rows(x, "x", ROW_TYPES)
-        rows, d = shape = x.shape
-        device = x.device
+        rows, d, x_stride = self._rows(x, "x", ROW_TYPES)
+        shape, device = (rows, d), x.device
         self._flat(gamma, "gamma", torch.bfloat16, d)
         res_stride = out_stride = y_stride = res_type = 0
         if residual is not None:
-            res_stride = self._rows(residual, "residual", ROW_TYPES, shape)
+            _, _, res_stride = self._rows(residual, "residual", ROW_TYPES, shape)
             if residual_out is None:
                 residual_out = torch.empty_strided(shape, (d, 1), dtype=residual.dtype, device=device)
                 out_stride = d
             else:
-                out_stride = self._rows(residual_out, "residual_out", (residual.dtype,), shape)
+                _, _, out_stride = self._rows(residual_out, "residual_out", (residual.dtype,), shape)
             res_type = ROW_TYPES[residual.dtype]
         elif residual_out is not None:
             raise ValueError("residual_out without a residual")
         codes, codes_stride, scales = self._new_codes(rows, d, codes, scales, device)
         if y is not None:
-            y_stride = self._rows(y, "y", (torch.bfloat16,), shape)
+            _, _, y_stride = self._rows(y, "y", (torch.bfloat16,), shape)
         elif want_y:
             y, y_stride = torch.empty_strided(shape, (d, 1), dtype=torch.bfloat16, device=device), d
         if rows > 0:
@@ -548,8 +548,7 @@ class MlaDecode:
         if stream is not None:
             with self._outputs_on(stream):
                 return self.quantize_rows(x, codes, scales)
-        x_stride = self._rows(x, "x", ROW_TYPES)
-        rows, d = x.shape
+        rows, d, x_stride = self._rows(x, "x", ROW_TYPES)
         codes, codes_stride, scales = self._new_codes(rows, d, codes, scales, x.device)
         if rows > 0:
             args = QUANTIZE_ARGS.pack(rows, d, ROW_TYPES[x.dtype], x.data_ptr(), x_stride, codes.data_ptr(),
@@ -565,17 +564,15 @@ class MlaDecode:
         if stream is not None:
             with self._outputs_on(stream):
                 return self.linear_q8(codes, scales, w_codes, w_scales, out, out_dtype)
-        a_stride = self._rows(codes, "codes", _INT8)
-        rows, k = codes.shape
-        w_stride = self._rows(w_codes, "w_codes", _INT8)
-        n, w_k = w_codes.shape
+        rows, k, a_stride = self._rows(codes, "codes", _INT8)
+        n, w_k, w_stride = self._rows(w_codes, "w_codes", _INT8)
         if w_k != k:
             raise ValueError(f"w_codes: expected [n, {k}], got {_shape(w_codes)}")
         self._flat(scales, "scales", torch.float32, rows)
         self._flat(w_scales, "w_scales", torch.float32, n)
         if out is not None:
             out_dtype = out.dtype
-            out_stride = self._rows(out, "out", ROW_TYPES, (rows, n))
+            _, _, out_stride = self._rows(out, "out", ROW_TYPES, (rows, n))
         else:
             if out_dtype not in ROW_TYPES:
                 raise ValueError(f"out_dtype: expected torch.bfloat16 or torch.float32, got {out_dtype}")
@@ -593,8 +590,8 @@ class MlaDecode:
 
     def _append_rows(self, call, x, gamma, cache, cache_type, exps, kv_lens, row_starts, page_table, eps, stream):
         """The checks and the call that append_rows and append_rows_fp8 share (exps: a quantised cache)."""
-        x_stride = self._rows(x, "x", ROW_TYPES)
-        if x.shape[1] != ROW:
+        rows, d, x_stride = self._rows(x, "x", ROW_TYPES)
+        if d != ROW:
             raise ValueError(f"x: expected [rows, {ROW}], got {_shape(x)}")
         self._flat(gamma, "gamma", torch.bfloat16, D_LATENT)
         B = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
@@ -631,7 +628,6 @@ class MlaDecode:
                 raise ValueError(f"exps: expected a contiguous int8 {tuple(sizes[:2])} tensor indexed as codes is, "
                                  f"got {_shape(exps)}")
             k_r, kv_exp = 0, exps.data_ptr()
-        rows = x.shape[0]
         if rows > 0:
             args = ROWS_ARGS.pack(B, rows, ROW_TYPES[x.dtype], eps, x.data_ptr(), x_stride, gamma.data_ptr(), c_kv, k_r,
                                   kv_exp, row_stride, seq_stride, kv_lens.data_ptr(),

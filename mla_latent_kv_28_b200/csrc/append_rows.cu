@@ -15,10 +15,11 @@
 // rows into a bf16 cache 26.0 us (5800 GB/s), into an E4M3 cache 26.1 us; 64 rows 2.4 us.
 //
 // The angle p theta_m is kept as an integer part of a turn (p times the frequency's 64-bit fraction,
-// which drops whole turns by itself): positions to 2^30 lose 2^-34 of a turn, and nothing but one
-// conversion to fp32 is left for the units of fp64 and conversions, which bound an earlier form. A
-// quantised row's exponent is read off the bits of its largest fp32 value; next to the border between
-// two exponents the row is taken again in fp64, so that the exponent is the one of the definition.
+// which drops whole turns by itself): positions to 2^30 lose 2^-34 of a turn, beside 2^-25 by the
+// rounding of the frequency as an fp64 number, and nothing but one conversion to fp32 is left for the
+// units of fp64 and conversions, which bound an earlier form. A quantised row's exponent is read off
+// the bits of its largest fp32 value; next to the border between two exponents the row is taken again
+// in fp64, so that the exponent is the one of the definition.
 #include <type_traits>
 
 #include "mla_internal.cuh"

@@ -160,8 +160,9 @@ int mla_decode_create(const mla_config_t* cfg, int device, mla_handle_t* out) {
     const double t = h->theta[m] / 6.283185307179586476925;
     turns[m] = (uint64_t)std::ldexp(t - std::floor(t), 64);
   }
+  // (waited for: streams that do not synchronise with the default one may read it right away)
   if (cudaMemcpy(h->ws.turns, turns, sizeof(turns), cudaMemcpyHostToDevice) != cudaSuccess ||
-      mla::init_linear_q8(*h) != cudaSuccess) {
+      cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess || mla::init_linear_q8(*h) != cudaSuccess) {
     cudaFree(base);
     delete h;
     return MLA_ERR_CUDA;

@@ -8,8 +8,8 @@
 // operand) times up to 128 tokens (N); its CTAs share the sum's length, each streaming its part of the
 // weights through a ring of TMA boxes into tcgen05 MMAs (kind::i8, int32 in tensor memory). Each CTA then
 // sends its partial sums to the CTAs that finish them (asynchronous stores into their shared memory,
-// counted by a barrier there: no second meeting), which add, scale and store. 33 x 16384 -> 5120 17.7 us
-// (4700 GB/s), 64 x 1536 -> 16384 7.8 us, 1 x 5120 -> 2112 4.7 us (2 us of launch, 1.5 us until the boxes
+// counted by a barrier there: no second meeting), which add, scale and store. 33 x 16384 -> 5120 16.8 us
+// (5000 GB/s), 64 x 1536 -> 16384 7.8 us, 1 x 5120 -> 2112 4.9 us (2 us of launch, 1.5 us until the boxes
 // are here and multiplied, 1 us of exchange).
 //
 // More tokens (linear_many): bound by the tensor core, and by the power that it takes. A pair of CTAs
@@ -62,6 +62,8 @@ __device__ __forceinline__ bool wait_ring(uint32_t bar, uint32_t parity, const W
 struct FewParams {
   int rows, n, n_tile, splits, kblocks, stages;
   uint32_t ring;         // bytes of the ring
+  uint32_t recip;        // ceil(2^18 / splits)
+  uint32_t pitch;        // bytes between a part's groups of four tokens: 16 for each of its channels
   uint32_t idesc;
   const float* a_scale;
   const float* w_scale;
@@ -94,8 +96,9 @@ __device__ __forceinline__ OT get_one(const uint8_t* box, int row, int col) {
 
 // smem: the barriers, the scales, a ring of stages [128 x 128 weight box | n_tile x 128 token box], the
 // partial sums that this CTA receives. Of the tile's 128 channels CTA r of the cluster finishes those from
-// ceil(128 r / splits) on: it gets from each CTA [its channels][4 tokens] pieces of 16 bytes, a
-// channel's pieces an odd number of 16-byte units from the next one's (no bank conflicts).
+// ceil(128 r / splits) on: it gets from each CTA pieces of 16 bytes, [4 tokens][its channels], so that what
+// a warp sends at a time, and what one reads, is contiguous (128 x 16384 -> 5120 22.8 us; with a channel's
+// tokens together 24.4, 64 x 5120 -> 2112 7.0 and 8.0 us).
 // kTiles: the tokens are cut into tiles too, one for each blockIdx.y (of its own, because the kernel of a few
 // microseconds was up to 0.7 us slower with the tile's offset in it: 128 x 1536 -> 16384).
 template <typename OT, bool kTiles>
@@ -114,13 +117,14 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
   const uint32_t ring = sbase + 2048, parts = ring + p.ring;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int splits = p.splits, rank = splits > 1 ? (int)cluster_ctarank() : 0;
-  const int f0 = (blockIdx.x / splits) * 128, t0 = kTiles ? blockIdx.y * p.n_tile : 0;
-  const int kb0 = (int)((int64_t)p.kblocks * rank / splits), kb1 = (int)((int64_t)p.kblocks * (rank + 1) / splits);
+  // x / splits for x <= 2^13 (kblocks is 1024 at most, splits 8): 2^18 / splits rounded up is close enough
+  const auto share = [&](int x) { return (int)((uint32_t)x * p.recip >> 18); };
+  const int f0 = (int)cluster_id_x() * 128, t0 = kTiles ? blockIdx.y * p.n_tile : 0;
+  const int kb0 = share(p.kblocks * rank), kb1 = share(p.kblocks * (rank + 1));
   const uint32_t tmem_cols = p.n_tile <= 32 ? 32u : p.n_tile <= 64 ? 64u : 128u;
   const int rows = kTiles ? min(p.n_tile, p.rows - t0) : p.rows, quads = (rows + 3) / 4;
-  const int c_begin = (128 * rank + splits - 1) / splits, c_count = (128 * (rank + 1) + splits - 1) / splits - c_begin;
-  const uint32_t pitch = (uint32_t)(quads | 1) * 16;          // bytes between a part's channels
-  const uint32_t part = (uint32_t)((128 + splits - 1) / splits) * pitch;   // ... between the parts
+  const int c_begin = share(128 * rank + splits - 1), c_count = share(128 * (rank + 1) + splits - 1) - c_begin;
+  const uint32_t part = (uint32_t)quads * p.pitch;   // bytes between the parts
   const WaitGuard guard{abort_flag, p.err, kErrTimeout, kWaitLimit};
 
   if (tid == 0) {
@@ -210,15 +214,15 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
           store1(out + j * p.out_stride, (float)(int32_t)r[j] * w * a_scale[c0 + j]);
     }
   } else {
-    const int owner = f * splits >> 7, c = f - (128 * owner + splits - 1) / splits;
+    const int owner = f * splits >> 7, c = f - share(128 * owner + splits - 1);
     cluster_wait();   // the others have set their barriers up
-    const uint32_t to = map_to_rank(parts + rank * part + c * pitch, owner), bar = map_to_rank(received, owner);
+    const uint32_t to = map_to_rank(parts + rank * part + c * 16, owner), bar = map_to_rank(received, owner);
     for (int c0 = 16 * (warp >> 2); c0 < rows; c0 += 32) {
       uint32_t r[16];
       tmem_ld16_sync(lanes | (tmem + c0), r);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (c0 + 4 * j < rows) st_async_v4(to + (c0 / 4 + j) * 16, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3], bar);
+        if (c0 + 4 * j < rows) st_async_v4(to + (c0 / 4 + j) * p.pitch, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3], bar);
     }
     ok = wait_bounded(received, 0, guard, true) && ok;
     const int count = min(c_count, p.n - f0 - c_begin);   // may be negative
@@ -226,7 +230,7 @@ linear_few(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ C
       for (int it = tid; it < count * quads; it += 256) {
         const int q = it / count, ch = it - q * count, col = f0 + c_begin + ch;
         int32_t acc[4] = {0, 0, 0, 0};
-        const uint8_t* from = smem + (parts - sbase) + ch * pitch + q * 16;
+        const uint8_t* from = smem + (parts - sbase) + ch * 16 + q * p.pitch;
         for (int src = 0; src < splits; ++src) {
           const int4 v = *reinterpret_cast<const int4*>(from + src * part);
           acc[0] += v.x; acc[1] += v.y; acc[2] += v.z; acc[3] += v.w;
@@ -554,7 +558,7 @@ FewShape few_shape(const mla_decode_s& h, const LinearArgs& a) {
   for (int splits = row_tiles > 1 ? 2 : 1; splits <= kMaxSplits && (splits == 1 || kblocks >= 2 * splits); ++splits)
     for (const bool two : {false, true}) {
       const uint32_t channels = (128 + splits - 1) / splits;   // of a CTA, at most
-      const uint32_t parts = splits == 1 ? 0 : splits * channels * (((uint32_t)n_tile / 4) | 1) * 16;
+      const uint32_t parts = splits == 1 ? 0 : splits * channels * ((uint32_t)n_tile / 4) * 16;
       const int per = (kblocks + splits - 1) / splits;
       const uint32_t limit = two ? kFewSmem : kFewSmemOne;
       if (limit < parts + kFewHead + stage) continue;
@@ -570,7 +574,7 @@ FewShape few_shape(const mla_decode_s& h, const LinearArgs& a) {
       if (clusters < 1) continue;
       const int64_t waves = (tiles + clusters - 1) / clusters, at_once = std::min<int64_t>(tiles, clusters);
       const int64_t arrival = waves * per * (int64_t)(stage / 110) * (at_once > one ? 10 + n_tile / 8 : 10) / 10;
-      const int64_t rest = (row_tiles > 1 ? 2100 : 1600) + waves * 1400 + (splits > 1 ? 340 + 30 * n_tile : 10 * n_tile);
+      const int64_t rest = (row_tiles > 1 ? 2300 : 1600) + waves * 1400 + (splits > 1 ? 340 + 18 * n_tile : 10 * n_tile);
       if (arrival + rest >= best.ns) continue;
       best = f;
       best.ns = arrival + rest;
@@ -590,6 +594,8 @@ cudaError_t launch_few(const mla_decode_s& h, const LinearArgs& a, const FewShap
   p.splits = f.splits;
   p.stages = f.stages;
   p.ring = f.ring;
+  p.recip = ((1u << 18) + f.splits - 1) / f.splits;
+  p.pitch = (128 + f.splits - 1) / f.splits * 16;
   CUtensorMap tw, ta;
   if (!encode(&tw, a.w_codes, (uint64_t)a.n, (uint64_t)a.k, (uint64_t)a.w_stride, 128) ||
       !encode(&ta, a.codes, (uint64_t)a.rows, (uint64_t)a.k, (uint64_t)a.codes_stride, (uint32_t)p.n_tile))
@@ -619,7 +625,7 @@ ManyShape many_shape(const mla_decode_s& h, const LinearArgs& a) {
     // cycles, as measured: a k block of a tile (2 x tile of them are the MMAs' at tile 256; narrower tiles
     // read as many tokens for less), and its results' way out, beside the next tile's sum but for the last
     const int64_t sum = kblocks * (220 + 14 * tile / 10), store = 400 + (tile + 63) / 64 * 850;
-    const int64_t ns = 4000 + (rounds * std::max(sum, store) + std::min(sum, store)) * 4 / 7;
+    const int64_t ns = 3800 + (rounds * std::max(sum, store) + std::min(sum, store)) * 4 / 7;
     if (ns < best.ns) best = ManyShape{tile, ns};
   }
   return best;
@@ -691,8 +697,8 @@ cudaError_t init_linear_q8(mla_decode_s& h) {
 cudaError_t launch_linear_q8(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s) {
   // Up to 64 tokens always linear_few (a pair's tile of 256 is mostly empty); of more, the one that should
   // be done first: few channels under a long sum are one pair's work for long, while clusters share it
-  // (us, linear_few against linear_many: 491 x 14864 -> 172 12.2 and 27.3, 128 x 1536 -> 16384 8.8 and 10.1,
-  // 195 x 15913 -> 2655 29 and 44; 512 x 5120 -> 2112 17 and 12.2, 2821 x 192 -> 1520 9.4 and 6.2).
+  // (us, linear_few against linear_many: 491 x 14864 -> 172 10.6 and 27.3, 128 x 1536 -> 16384 8.8 and 10.1,
+  // 195 x 15913 -> 2655 23 and 36; 512 x 5120 -> 2112 15 and 11.7, 2821 x 192 -> 1520 9.4 and 6.2).
   const FewShape f = few_shape(h, a);
   const ManyShape m = a.rows <= 64 ? ManyShape{} : many_shape(h, a);
   if (f.capped_ns < m.ns) return a.out_f32 ? launch_few<float>(h, a, f, s) : launch_few<__nv_bfloat16>(h, a, f, s);

@@ -471,7 +471,9 @@ MLA_API int mla_append_rows(mla_handle_t h, const mla_append_rows_t* args, mla_s
 
 /*
  * mla_append_rows into a quantised cache (codes and exponents as mla_append_kv_fp8 writes them: the
- * smallest power of two with max|row| / 2^e <= 448, values rounded to the nearest E4M3 code).
+ * smallest power of two with max|row| / 2^e <= 448, e in -126..127 and 0 for an all-zero row, values
+ * rounded to the nearest E4M3 code). A NaN becomes a NaN code and counts for no exponent; a row with an
+ * infinity gets 127 and the infinity the largest code.
  */
 MLA_API int mla_append_rows_fp8(mla_handle_t h, const mla_append_rows_t* args, mla_stream_t stream);
 

@@ -270,7 +270,7 @@ append_rows_kernel(const RowsParams p) {
       const int f = exact_exponent<XT, G>(x, p.gamma, p.eps, p.turns, position, l);
       if (border) e = f;
     }
-    e = bits == 0 ? 0 : min(max(e, -126), 127);
+    e = bits == 0 ? 0 : bits == 0x7F800000u ? 127 : min(max(e, -126), 127);   // (an infinity: the largest)
     if (row < 0) return;
     const float q = exp2f((float)-e);
     uint8_t* out = p.codes + row * p.cv.row_stride;

@@ -231,15 +231,22 @@ norm_q8_kernel(const NormParams p) {
   float rstd = 1.f;
   if constexpr (kNorm) {
     rstd = 1.f / sqrtf(ss / (float)p.d + p.eps);
-    if (wide && dd != 0.0) rstd = (float)(1.0 / sqrt((dd + (double)ss) / p.d + (double)p.eps));
+    // Without an eps 1 / rms of a row of subnormal values lies beyond fp32: minus 2^-64 times it stands for
+    // it, and the 2^64 go onto t and m by themselves (exact)
+    if (wide && dd != 0.0) {
+      const double exact = 1.0 / sqrt((dd + (double)ss) / p.d + (double)p.eps);
+      rstd = (float)(exact > 0x1p100 ? exact * -0x1p-64 : exact);
+    }
     if (p.y != nullptr) {
       __nv_bfloat16* y = p.y + row * p.y_stride;
+      const float up = rstd < 0.f ? 0x1p64f : 1.f;
+      const float2 by = make_float2(fabsf(rstd), fabsf(rstd));
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
         const int e = W * (8 / W * n * nthr + tid);
         float2 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = sm100::fmul2(t[n][i], make_float2(rstd, rstd));
+        for (int i = 0; i < 4; ++i) v[i] = sm100::fmul2(sm100::fmul2(t[n][i], make_float2(up, up)), by);
         store_pairs<W>(y + e, step, d - e, v);
       }
     }
@@ -248,7 +255,8 @@ norm_q8_kernel(const NormParams p) {
   float m = __uint_as_float(mb);
   const bool finite = mb < 0x7F800000u;
   if (tid == 0 && d > 0)
-    p.scales[row] = !finite ? __uint_as_float(0x7FC00000u) : m > 0.f ? m * rstd / 127.f : 0.f;
+    p.scales[row] = !finite ? __uint_as_float(0x7FC00000u)
+                    : m > 0.f ? (rstd < 0.f ? m * 0x1p64f * -rstd : m * rstd) / 127.f : 0.f;
   // below 1e-30, where 127 / m may overflow, the row is scaled up by a power of two (exact)
   float lift = 1.f;
   if (m < 1e-30f) {

@@ -108,7 +108,9 @@ __device__ __forceinline__ T group_max(T v) {
   return v;
 }
 
-// 1 / sqrt(mean square + eps) of a row in fp64 (lane l of G; the whole warp takes part).
+// 1 / sqrt(mean square + eps) of a row in fp64 (lane l of G; the whole warp takes part). Without an eps that of
+// a row of subnormal values lies beyond fp32: it comes as minus 2^-64 times it, and the caller puts the
+// 2^64 on the values (exact).
 template <typename XT, int G>
 __device__ __noinline__ float wide_rstd(const XT* x, float eps, int l) {
   double ss = 0.0;
@@ -116,7 +118,8 @@ __device__ __noinline__ float wide_rstd(const XT* x, float eps, int l) {
     const double v = load1(x + f);
     ss = fma(v, v, ss);
   }
-  return (float)(1.0 / sqrt(group_sum<G>(ss) / kDLatent + (double)eps));
+  const double rstd = 1.0 / sqrt(group_sum<G>(ss) / kDLatent + (double)eps);
+  return (float)(rstd > 0x1p100 ? rstd * -0x1p-64 : rstd);
 }
 
 // A quantised row's exponent with the whole row in fp64, its angles at `position` (as above).
@@ -245,6 +248,20 @@ append_rows_kernel(const RowsParams p) {
     gamma.load(p.gamma + 8 * (l + G * c), 0, 1);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[c][j] = sm100::fmul2(sm100::fmul2(raw[c].pair(j), make_float2(rstd, rstd)), gamma.pair(j));
+  }
+  if (rstd < 0.f) {   // (read again: kept, the values cost registers that rows in earnest pay for)
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      Raw8<XT, 8> again;
+      Raw8<__nv_bfloat16, 8> gamma;
+      again.load(x + 8 * (l + G * c), 0, 1);
+      gamma.load(p.gamma + 8 * (l + G * c), 0, 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 r = sm100::fmul2(again.pair(j), make_float2(0x1p64f, 0x1p64f));
+        v[c][j] = sm100::fmul2(sm100::fmul2(r, make_float2(-rstd, -rstd)), gamma.pair(j));
+      }
+    }
   }
   if constexpr (!kFp8) {
     if (row < 0) return;

@@ -108,6 +108,7 @@ MLA_API int mla_check_config(const mla_config_t* cfg);
  * Create a handle on CUDA device `device` and allocate its workspace there (sized from
  * cfg->max_batch, cfg->max_kv_len and n_heads). On success *out is the handle and the
  * return is MLA_OK; on failure *out is NULL. Makes `device` current on the calling thread.
+ * The handle is ready for any stream on return; other work on the device is not waited for.
  */
 MLA_API int mla_decode_create(const mla_config_t* cfg, int device, mla_handle_t* out);
 

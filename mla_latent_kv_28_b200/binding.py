@@ -460,11 +460,14 @@ class MlaDecode:
         """The stream to launch on: the current one of the handle's device unless given."""
         return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else stream.cuda_stream
 
+    def _own_stream(self, stream) -> None:
+        if stream is not None and stream.device.index != self.device:
+            raise ValueError(f"stream: expected one of cuda:{self.device}, got one of {stream.device}")
+
     def _outputs_on(self, stream):
         """For a call on a stream that need not be the current one: tensors that the call makes belong to
         the stream that writes them (memory freed on the current one may still be in use there)."""
-        if stream.device.index != self.device:
-            raise ValueError(f"stream: expected one of cuda:{self.device}, got one of {stream.device}")
+        self._own_stream(stream)
         return torch.cuda.stream(stream)
 
     def _rows(self, t: torch.Tensor, name: str, dtypes, shape=None) -> Tuple[int, int, int]:
@@ -590,6 +593,7 @@ class MlaDecode:
 
     def _append_rows(self, call, x, gamma, cache, cache_type, exps, kv_lens, row_starts, page_table, eps, stream):
         """The checks and the call that append_rows and append_rows_fp8 share (exps: a quantised cache)."""
+        self._own_stream(stream)
         rows, d, x_stride = self._rows(x, "x", ROW_TYPES)
         if d != ROW:
             raise ValueError(f"x: expected [rows, {ROW}], got {_shape(x)}")

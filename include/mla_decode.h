@@ -441,7 +441,7 @@ MLA_API int mla_linear_q8(mla_handle_t h, const mla_linear_q8_t* args, mla_strea
  * n_rows     rows of x (>= 0)
  * x          [n_rows, 576] of x_type, 16-byte aligned, x_stride * element size a multiple of 16
  * row_starts int32 [batch + 1], not decreasing; NULL: q_len rows per sequence in order
- *            (n_rows = batch * q_len)
+ *            (n_rows = batch * q_len, or 0)
  * gamma, rms_eps, the cache, kv_lens, page_table: as for mla_append_kv. No two rows may go to the
  *            same cache row. k_r needs c_kv's alignment.
  * A row whose position lies before 0, whose kv_lens entry is over max_kv_len, or whose page-table

@@ -548,7 +548,7 @@ int append_rows_common(mla_handle_t h, const mla_append_rows_t* a, bool fp8, mla
       (fp8 ? a->kv_exp == nullptr : a->k_r == nullptr) || a->kv_lens == nullptr)
     return MLA_ERR_INVALID_ARG;
   if (a->batch < 1 || a->batch > h->cfg.max_batch || a->n_rows < 0) return MLA_ERR_INVALID_ARG;
-  if (a->row_starts == nullptr && a->n_rows != a->batch * h->q_len) return MLA_ERR_INVALID_ARG;
+  if (a->row_starts == nullptr && a->n_rows != 0 && a->n_rows != a->batch * h->q_len) return MLA_ERR_INVALID_ARG;
   const int xb = type_bytes(a->x_type);
   if (xb == 0 || a->x_stride < mla::kRow || a->x_stride * xb % 16 != 0 || !aligned16(a->x) || !aligned16(a->gamma))
     return MLA_ERR_INVALID_ARG;

@@ -16,7 +16,7 @@
 // A group of threads takes a row: 8, 16 or 32 lanes up to 1024 values, a block of its own beyond. A
 // thread holds NV vectors of 8 values of t (neighbours where rows are 16-byte aligned) and nothing
 // else across the reduction. Bound by HBM: per value the bytes of x, the residual in and out, one
-// code, and y where it is wanted; rows of bf16 without a residual also by the issue slots (10
+// code, and y where it is wanted; rows of bf16 without a residual also by the issue slots (11
 // instructions per value with packed fp32 pairs and two- and three-way maxima). Measured: 4096 x 5120
 // bf16 with an fp32 residual and y 42.4 us (6430 GB/s); 2048 x 16384 bf16 quantised 19.8 us (5090 GB/s),
 // the same in fp32 26.3 us (6390 GB/s); one row of 5120 2.1 us, the launch and one round trip. Rows of odd
@@ -232,21 +232,34 @@ norm_q8_kernel(const NormParams p) {
   if constexpr (kNorm) {
     rstd = 1.f / sqrtf(ss / (float)p.d + p.eps);
     // Without an eps 1 / rms of a row of subnormal values lies beyond fp32: minus 2^-64 times it stands for
-    // it, and the 2^64 go onto t and m by themselves (exact)
+    // it, and the 2^64 go onto t and m by themselves (exact): with another product for y, or in place for
+    // odd widths, whose kernels have no registers left (13000 x 1537 fp32, bf16 residual 79.5 us with the
+    // product, 74.0 in place, 72.8 without either; 4096 x 5120 bf16 16.5, 17.1 and 16.4).
     if (wide && dd != 0.0) {
       const double exact = 1.0 / sqrt((dd + (double)ss) / p.d + (double)p.eps);
       rstd = (float)(exact > 0x1p100 ? exact * -0x1p-64 : exact);
     }
+    if constexpr (W == 1) {
+      if (rstd < 0.f) {
+        rstd = -rstd;
+        if (mb < 0x7F800000u) mb = __float_as_uint(__uint_as_float(mb) * 0x1p64f);
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[n][i] = make_float2(t[n][i].x * 0x1p64f, t[n][i].y * 0x1p64f);
+      }
+    }
     if (p.y != nullptr) {
       __nv_bfloat16* y = p.y + row * p.y_stride;
       const float up = rstd < 0.f ? 0x1p64f : 1.f;
-      const float2 by = make_float2(fabsf(rstd), fabsf(rstd));
+      const float size = W == 1 ? rstd : fabsf(rstd);
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
         const int e = W * (8 / W * n * nthr + tid);
         float2 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = sm100::fmul2(sm100::fmul2(t[n][i], make_float2(up, up)), by);
+        for (int i = 0; i < 4; ++i)
+          v[i] = sm100::fmul2(W == 1 ? t[n][i] : sm100::fmul2(t[n][i], make_float2(up, up)), make_float2(size, size));
         store_pairs<W>(y + e, step, d - e, v);
       }
     }
@@ -256,7 +269,7 @@ norm_q8_kernel(const NormParams p) {
   const bool finite = mb < 0x7F800000u;
   if (tid == 0 && d > 0)
     p.scales[row] = !finite ? __uint_as_float(0x7FC00000u)
-                    : m > 0.f ? (rstd < 0.f ? m * 0x1p64f * -rstd : m * rstd) / 127.f : 0.f;
+                    : m > 0.f ? (W > 1 && rstd < 0.f ? m * 0x1p64f * -rstd : m * rstd) / 127.f : 0.f;
   // below 1e-30, where 127 / m may overflow, the row is scaled up by a power of two (exact)
   float lift = 1.f;
   if (m < 1e-30f) {
@@ -297,7 +310,9 @@ cudaError_t launch_shape(const NormParams& p, cudaStream_t s) {
   }
 }
 
-// Rows with less than 16-byte alignment.
+// Rows with less than 16-byte alignment. Four values at a time against two: 1200 x 16380 bf16 with an fp32
+// residual and y 44.7 and 52.0 us, 4882 x 4100 bf16 quantised 15.9 and 16.9; two against one: 10000 x 1022
+// with the residual and y 22.4 and 37.3 us, 2441 x 8194 bf16 quantised 18.7 and 51.0.
 template <typename XT, typename RT, bool kNorm, int W>
 cudaError_t launch_narrow(const NormParams& p, cudaStream_t s) {
   if (p.d <= 256) return launch_shape<XT, RT, kNorm, 1, W, 32>(p, s);

@@ -12,11 +12,13 @@
 // (5000 GB/s), 64 x 1536 -> 16384 7.8 us, 1 x 5120 -> 2112 4.9 us (2 us of launch, 1.5 us until the boxes
 // are here and multiplied, 1 us of exchange).
 //
-// More tokens (linear_many): bound by the tensor core, and by the power that it takes. A pair of CTAs
-// (cta_group::2) takes 256 tokens x up to 256 channels: each CTA holds 128 of the tokens and half of the
-// channels, so a pair reads 64 KB per 128 steps of k for 256 x 256 results. Persistent, with the
-// accumulator double-buffered in tensor memory: eight warps scale and store a tile while the next is
-// summed. 2048 x 16384 -> 5120 115 us (2980 TOP/s; 135 us at the clocks of a long run), 8192 x 512 -> 8192
+// More tokens (linear_many): bound by the tensor core, and by the power that it takes, where tokens and sums
+// are long; between 129 and some 2000 tokens by what tiles of 256 tokens in whole rounds over the pairs
+// leave idle, and by set-up (512 x 5120 -> 2112 11.9 us for 3.3 us of products, 1048 x 7376 -> 5576 at least
+// 49.5 for 25.7). A pair of CTAs (cta_group::2) takes 256 tokens x up to 256 channels: each CTA holds 128 of
+// the tokens and half of the channels, so a pair reads 64 KB per 128 steps of k for 256 x 256 results.
+// Persistent, with the accumulator double-buffered in tensor memory: eight warps scale and store a tile
+// while the next is summed. 2048 x 16384 -> 5120 115 us (2980 TOP/s; 135 us at the clocks of a long run), 8192 x 512 -> 8192
 // 40 us (its 134 MB of results), 333 x 1000 -> 777 6 to 8 us.
 //
 // In both the loops that issue copies and MMAs are run by whole warps with one elected lane, so that
@@ -695,9 +697,11 @@ cudaError_t init_linear_q8(mla_decode_s& h) {
 }
 
 cudaError_t launch_linear_q8(const mla_decode_s& h, const LinearArgs& a, cudaStream_t s) {
-  // Up to 64 tokens always linear_few (a pair's tile of 256 is mostly empty); of more, the one that should
-  // be done first: few channels under a long sum are one pair's work for long, while clusters share it
-  // (us, linear_few against linear_many: 491 x 14864 -> 172 10.6 and 27.3, 128 x 1536 -> 16384 8.8 and 10.1,
+  // Up to 64 tokens always linear_few, a pair's tile of 256 being mostly empty (it was ahead for every one of
+  // nine weights, 512 -> 512, 64 -> 131072 and 2048 -> 128 among them: 1 x 5120 -> 2112 4.9 us against 17.5,
+  // 64 x 16384 -> 5120 18.2 against 27.8, 64 x 512 -> 512 3.7 against 3.9); of more, the one that should be
+  // done first: few channels under a long sum are one pair's work for long, while clusters share it (us,
+  // linear_few against linear_many: 491 x 14864 -> 172 10.6 and 27.3, 128 x 1536 -> 16384 8.8 and 10.1,
   // 195 x 15913 -> 2655 23 and 36; 512 x 5120 -> 2112 15 and 11.7, 2821 x 192 -> 1520 9.4 and 6.2).
   const FewShape f = few_shape(h, a);
   const ManyShape m = a.rows <= 64 ? ManyShape{} : many_shape(h, a);

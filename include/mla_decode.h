@@ -344,7 +344,8 @@ enum {
  *   rstd   = 1 / sqrt(mean(r^2) + rms_eps)
  *   t      = r * gamma (fp32);  y = t * rstd                                       (bf16)
  *   codes  = the integers nearest to 127 t / m, ties to even, m = max|t|
- *   scales = m * rstd / 127, so that codes * scales is the normalised row to half a code
+ *   scales = m * rstd / 127, so that codes * scales is the normalised row to half a code (to the
+ *            scale's own rounding where that is a subnormal number, under 2^-126)
  * A row of zeros gets codes 0 and scale 0; a row with an infinity or a NaN in t gets codes 0 and a
  * NaN scale. Codes depend on no sum: they are the same on every run and for any layout.
  * d             1..16384

@@ -625,7 +625,8 @@ ManyShape many_shape(const mla_decode_s& h, const LinearArgs& a) {
   for (int tile = 256; tile >= 32; tile -= 32) {
     const int64_t tiles = tiles_m * ((a.n + tile - 1) / tile), rounds = (tiles + clusters - 1) / clusters;
     // cycles, as measured: a k block of a tile (2 x tile of them are the MMAs' at tile 256; narrower tiles
-    // read as many tokens for less), and its results' way out, beside the next tile's sum but for the last
+    // read as many tokens for less), and its results' way out, beside the next tile's sum but for the last;
+    // in ns at 1.75 GHz (the longest products run at less, where linear_few is no choice)
     const int64_t sum = kblocks * (220 + 14 * tile / 10), store = 400 + (tile + 63) / 64 * 850;
     const int64_t ns = 3800 + (rounds * std::max(sum, store) + std::min(sum, store)) * 4 / 7;
     if (ns < best.ns) best = ManyShape{tile, ns};
